@@ -11,7 +11,8 @@ import os
 
 F16, BF16, F32, E4M3, E5M2 = 0, 1, 2, 3, 4
 STATUS_NAMES = {0: "GEMM_OK", 1: "GEMM_ERR_INVALID_ARG", 2: "GEMM_ERR_UNSUPPORTED",
-                3: "GEMM_ERR_CUDA", 4: "GEMM_ERR_OOM", 5: "GEMM_ERR_TIMEOUT"}
+                3: "GEMM_ERR_CUDA", 4: "GEMM_ERR_OOM", 5: "GEMM_ERR_TIMEOUT",
+                6: "GEMM_ERR_BAD_INDEX"}
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm.so")
 
 # Every function include/gemm.h declares (checked against the header by the tests).
@@ -20,7 +21,8 @@ EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_epilogue", "gemm
            "gemm_set_config",
            "gemm_last_config", "gemm_device_status", "gemm_set_wait_limit",
            "gemm_set_test_stall", "gemm_sm_count", "gemm_status_string", "gemm_run_noalloc",
-           "gemm_last_cuda_error", "gemm_plan")
+           "gemm_last_cuda_error", "gemm_plan",
+           "gemm_run_adapters", "gemm_rotary", "gemm_adjust_logits")
 
 
 class GemmConfig(ctypes.Structure):
@@ -47,6 +49,35 @@ class GemmBlockScales(ctypes.Structure):
     sfb per (128 rows, 128 of K) of B."""
     _fields_ = [("sfa", ctypes.c_void_p), ("sfb", ctypes.c_void_p), ("block_m", ctypes.c_int32),
                 ("block_n", ctypes.c_int32)]
+
+
+class GemmAdapters(ctypes.Structure):
+    """gemm_adapters_t: a pool of low-rank adapters, down count x rank x K and up
+    count x N x rank, with a factor for each."""
+    _fields_ = [("down", ctypes.c_void_p), ("up", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
+PAIRS_HALF, PAIRS_NEIGHBOURS = 0, 1
+
+
+class GemmRotary(ctypes.Structure):
+    """gemm_rotary_t: the tables, the tokens' positions along every axis, and which axis
+    turns which pair."""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("num_positions", ctypes.c_int64), ("axes", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("pairs", ctypes.c_int32),
+                ("inverse", ctypes.c_int32)]
+
+
+class GemmLogits(ctypes.Structure):
+    """gemm_logits_t: histories and penalties, biases and masks of a batch of rows."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("tokens", "token_start", "prompt_len", "repetition",
+                                                "frequency", "presence", "bias_tokens",
+                                                "bias_values", "bias_start", "mask")]
+                + [("mask_stride", ctypes.c_int64), ("mask_count", ctypes.c_int64),
+                   ("mask_row", ctypes.c_void_p)])
 
 
 class GemmProblem(ctypes.Structure):
@@ -117,6 +148,11 @@ def lib():
     L.gemm_run_blockwise.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, i32,
                                      ctypes.POINTER(GemmBlockScales), vp]
     L.gemm_run_grouped.argtypes = [vp, ctypes.POINTER(GemmProblem), i32, i32, i32, vp]
+    L.gemm_run_adapters.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, i32,
+                                    ctypes.POINTER(GemmAdapters), vp, vp]
+    L.gemm_rotary.argtypes = [vp, vp, vp] + [i64] * 7 + [i32, ctypes.POINTER(GemmRotary), vp]
+    L.gemm_adjust_logits.argtypes = [vp, vp, vp] + [i64] * 4 + [i32, i32,
+                                                                ctypes.POINTER(GemmLogits), vp]
     L.gemm_status_string.argtypes = [i32]
     L.gemm_status_string.restype = ctypes.c_char_p
     L.gemm_plan.argtypes = [ctypes.POINTER(GemmDeviceModel), ctypes.POINTER(GemmConfig), i64, i64,
@@ -144,10 +180,44 @@ def torch_float32():
     return torch.float32
 
 
+def torch_int32():
+    import torch
+    return torch.int32
+
+
 def torch_dtype_code(dt) -> int:
     import torch
     return {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32,
             torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}[dt]
+
+
+def _need(t, name, dtype, shape, device):
+    """Check an auxiliary tensor (None stays None) and give its address."""
+    if t is None:
+        return None
+    if (t.device != device or t.dtype != dtype or not t.is_contiguous()
+            or (shape is not None and tuple(t.shape) != tuple(shape))):
+        want = "" if shape is None else f" of shape {tuple(shape)}"
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor{want} on {device}")
+    return t.data_ptr()
+
+
+def pair_axes(sections, interleaved=False):
+    """The axis that turns each rotary pair, from the number of pairs of every axis: axis
+    after axis ([2, 1] -> 0 0 1), or dealt out in turn until an axis has its pairs
+    (interleaved; [2, 1] -> 0 1 0)."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0:
+        raise ValueError("sections must be numbers of pairs, one for each axis")
+    if not interleaved:
+        return [a for a, n in enumerate(left) for _ in range(n)]
+    axes = []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                left[a] -= 1
+                axes.append(a)
+    return axes
 
 
 def _stream_ptr(stream, device):
@@ -283,6 +353,113 @@ class Gemm:
                                       torch_dtype_code(dout),
                                       _stream_ptr(stream, problems[0][0].device))
         _check(code, f"gemm_run_grouped count={len(problems)}", self._h)
+
+    # ------------------------------------------ operators around the projections --
+    def run_adapters(self, X, W, Y, down, up, row_adapter, scale=None, stream=None):
+        """Y[i] = W @ X[i] + scale[a] * up[a] @ (down[a] @ X[i]) with a = row_adapter[i]
+        (no second term where a is negative): CUDA tensors X (M,K), W (N,K), Y (M,N), down
+        (adapters, rank, K), up (adapters, N, rank) of X's dtype, row_adapter int32 (M),
+        scale float32 (adapters) or None; all contiguous."""
+        if not (X.is_cuda and W.device == X.device and Y.device == X.device):
+            raise ValueError("X, W and Y must be CUDA tensors of one device")
+        if X.dim() != 2 or W.dim() != 2 or down.dim() != 3:
+            raise ValueError("X and W must be 2-D, down and up 3-D")
+        M, K = X.shape
+        N = W.shape[0]
+        count, rank = down.shape[:2]
+        _need(X, "X", X.dtype, (M, K), X.device)
+        _need(W, "W", X.dtype, (N, K), X.device)
+        _need(Y, "Y", Y.dtype, (M, N), X.device)
+        ad = GemmAdapters(_need(down, "down", X.dtype, (count, rank, K), X.device),
+                          _need(up, "up", X.dtype, (count, N, rank), X.device),
+                          _need(scale, "scale", torch_float32(), (count,), X.device), count, rank)
+        rows = _need(row_adapter, "row_adapter", torch_int32(), (M,), X.device)
+        code = lib().gemm_run_adapters(self._h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), M, N, K,
+                                       torch_dtype_code(X.dtype), torch_dtype_code(Y.dtype),
+                                       ctypes.byref(ad), rows, _stream_ptr(stream, X.device))
+        _check(code, f"gemm_run_adapters M={M} N={N} K={K} rank={rank}", self._h)
+        return Y
+
+    def rotary(self, x, y, cos, sin, positions, pair_axis=None, neighbours=False, inverse=False,
+               stream=None):
+        """Turn the pairs of every head by their tokens' positions: CUDA tensors x and y
+        (tokens, heads, dim) of one dtype, values of a head contiguous, any other strides,
+        y possibly x; cos and sin float32 (positions, pairs); positions int32 (axes, tokens)
+        or (tokens,); pair_axis the axis of every pair (see pair_axes; None: the first).
+        Pairs are (i, i + pairs), or neighbouring values.  inverse turns back (the
+        gradient)."""
+        if not (x.is_cuda and y.device == x.device and y.dtype == x.dtype and x.dim() == 3
+                and y.shape == x.shape):
+            raise ValueError("x and y must be CUDA tensors (tokens, heads, dim) of one device and dtype")
+        T, H, D = x.shape
+        if D > 1 and (x.stride(2) != 1 or y.stride(2) != 1):
+            raise ValueError("the values of a head must be contiguous")
+        if positions.dim() == 1:
+            positions = positions[None]
+        if cos.dim() != 2 or positions.dim() != 2:
+            raise ValueError("cos and sin must be (positions, pairs), positions (axes, tokens)")
+        half, axes = cos.shape[1], positions.shape[0]
+        axis_ptr = None
+        if pair_axis is not None:
+            if len(pair_axis) != half:
+                raise ValueError(f"pair_axis must name an axis for each of the {half} pairs")
+            if not all(0 <= a < axes for a in pair_axis):
+                raise ValueError(f"pair_axis must hold axes below {axes}")
+            axis_ptr = ctypes.cast((ctypes.c_uint8 * half)(*pair_axis), ctypes.c_void_p)
+        r = GemmRotary(_need(cos, "cos", torch_float32(), (cos.shape[0], half), x.device),
+                       _need(sin, "sin", torch_float32(), (cos.shape[0], half), x.device),
+                       _need(positions, "positions", torch_int32(), (axes, T), x.device),
+                       axis_ptr, cos.shape[0], axes, 2 * half,
+                       PAIRS_NEIGHBOURS if neighbours else PAIRS_HALF, 1 if inverse else 0)
+        code = lib().gemm_rotary(self._h, x.data_ptr(), y.data_ptr(), T, H, D, x.stride(0),
+                                 x.stride(1), y.stride(0), y.stride(1), torch_dtype_code(x.dtype),
+                                 ctypes.byref(r), _stream_ptr(stream, x.device))
+        _check(code, f"gemm_rotary tokens={T} heads={H} dim={D}", self._h)
+        return y
+
+    def adjust_logits(self, logits, out, tokens=None, token_start=None, prompt_len=None,
+                      repetition=None, frequency=None, presence=None, bias_tokens=None,
+                      bias_values=None, bias_start=None, mask=None, mask_row=None, stream=None):
+        """Penalties for repeated tokens, biases and grammar masks (gemm_adjust_logits):
+        CUDA tensors logits and out (rows, vocab), rows of any stride, out possibly logits.
+        tokens (int32) and token_start (int64, rows + 1) are the rows' histories, the first
+        prompt_len (int32) of each the prompt; repetition, frequency and presence float32
+        (rows); bias_tokens (int32, ascending within a row), bias_values (float32) and
+        bias_start (int64, rows + 1) the biases; mask int32 (masks, words) with bit
+        v % 32 of word v // 32 set where token v may follow, mask_row int32 (rows),
+        negative for no mask, or None for one mask per row."""
+        import torch
+        if not (logits.is_cuda and out.device == logits.device and logits.dim() == 2
+                and out.shape == logits.shape):
+            raise ValueError("logits and out must be CUDA tensors (rows, vocab) of one device")
+        B, V = logits.shape
+        if V > 1 and (logits.stride(1) != 1 or out.stride(1) != 1):
+            raise ValueError("the logits of a row must be contiguous")
+        dev, f32, i32, i64 = logits.device, torch.float32, torch.int32, torch.int64
+        if mask is not None and mask.dim() != 2:
+            raise ValueError("mask must be (masks, words)")
+        nb = None if bias_tokens is None else bias_tokens.shape
+        a = GemmLogits(_need(tokens, "tokens", i32, None, dev),
+                       _need(token_start, "token_start", i64, (B + 1,), dev),
+                       _need(prompt_len, "prompt_len", i32, (B,), dev),
+                       _need(repetition, "repetition", f32, (B,), dev),
+                       _need(frequency, "frequency", f32, (B,), dev),
+                       _need(presence, "presence", f32, (B,), dev),
+                       _need(bias_tokens, "bias_tokens", i32, None, dev),
+                       _need(bias_values, "bias_values", f32, nb, dev),
+                       _need(bias_start, "bias_start", i64, (B + 1,), dev),
+                       _need(mask, "mask", i32, None, dev),
+                       0 if mask is None else mask.shape[1], 0 if mask is None else mask.shape[0],
+                       _need(mask_row, "mask_row", i32, (B,), dev))
+        # (a single row's or column's stride says nothing)
+        sl, so = (max(t.stride(0), V) if B > 1 else V for t in (logits, out))
+        if B > 1 and (logits.stride(0) < V or out.stride(0) < V):
+            raise ValueError("rows must not overlap")
+        code = lib().gemm_adjust_logits(self._h, logits.data_ptr(), out.data_ptr(), B, V, sl, so,
+                                        torch_dtype_code(logits.dtype), torch_dtype_code(out.dtype),
+                                        ctypes.byref(a), _stream_ptr(stream, dev))
+        _check(code, f"gemm_adjust_logits rows={B} vocab={V}", self._h)
+        return out
 
     def run_host(self, A, B, C, dtype_in, dtype_out, stream=None):
         """gemm_run_host on CPU tensors (pinned for asynchronous copies)."""

@@ -12,6 +12,7 @@
 #include <new>
 #include <vector>
 
+#include "context.h"
 #include "gemm.h"
 #include "launch.h"
 #include "umma.cuh"
@@ -20,71 +21,12 @@ using namespace gb300;
 
 namespace {
 
-constexpr int kTmapCacheSize = 16;
 // A single row of A takes the matrix-vector path without being asked when K is at most
 // this (measured back to back, M = 1: 8192 x 8192 27.5 us against 28.9 on the tensor
 // cores, 28672 x 8192 74.5 against 81.4, 4096 x 4096 9.0 against 13.9, 14336 x 4096
 // 22.1 against 25.7; but 8192 x 28672 85.0 against 83.9, and with two or more rows of
 // A the tensor cores win: 2 x 8192 x 8192 30.4 against 28.7).
 constexpr int64_t kGemvAutoMaxK = 16384;
-
-struct TmapKey {
-  const void* ptr;
-  int64_t rows, cols;
-  int32_t dtype, box_rows;
-  bool operator==(const TmapKey& o) const {
-    return ptr == o.ptr && rows == o.rows && cols == o.cols && dtype == o.dtype &&
-           box_rows == o.box_rows;
-  }
-};
-
-struct TmapEntry {
-  TmapKey key;
-  CUtensorMap map;
-  bool valid;
-};
-
-}  // namespace
-
-struct gemm_ctx {
-  int device = 0;
-  cudaError_t last_cuda = cudaSuccess;  // the CUDA error behind the last GEMM_ERR_CUDA launch
-  int sms = 0;
-  uint32_t* d_status = nullptr;
-  float* d_ws = nullptr;
-  size_t ws_bytes = 0;
-  uint32_t* d_ctr = nullptr;
-  size_t ctr_count = 0;
-  void* d_stage[3] = {nullptr, nullptr, nullptr};  // gemm_run_host: A, B, C
-  size_t stage_bytes[3] = {0, 0, 0};
-  gemm_config_t forced = {};
-  gemm_config_t last = {};
-  uint64_t wait_limit_ns = 2000000000ull;
-  int32_t test_stall = 0;
-  TmapEntry cache[kTmapCacheSize] = {};
-  int cache_next = 0;
-  int resident[2][2][2][3] = {};  // [cta_group-1][bn==256][small A][out]: co-resident units (0: unknown)
-  // gemm_plan: a device described instead of queried (resident CTA pairs, and clusters of
-  // four CTAs for the pair's cluster K split); the GPU is never touched
-  bool model = false;
-  int model_pairs = 0, model_clusters4 = 0;
-  // grouped launches: a ring of problem tables (pinned host copy, device copy and the
-  // event that marks the host copy reusable)
-  static constexpr int kGroupRing = 4;
-  GroupDesc* h_groups[kGroupRing] = {};
-  GroupDesc* d_groups[kGroupRing] = {};
-  int32_t* h_gstart[kGroupRing] = {};
-  int32_t* d_gstart[kGroupRing] = {};
-  cudaEvent_t group_done[kGroupRing] = {};
-  size_t group_cap[kGroupRing] = {};
-  int group_next = 0;
-  // gemm_run_host: copy streams and the events that order the chunks of the pipeline
-  static constexpr int kHostChunks = 8;
-  cudaStream_t copy_in = nullptr, copy_out = nullptr;
-  cudaEvent_t host_ev[2 + 3 * kHostChunks] = {};
-};
-
-namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -101,11 +43,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 bool is_fp8(int d) { return d == GEMM_E4M3 || d == GEMM_E5M2; }
 
-// 2-D tensor map over a row-major rows x cols matrix, 128-byte swizzle, box of 128
-// bytes of columns x box_rows rows.  Loads read out-of-range elements as zero (M, N and
-// K tails); stores skip them.
-bool make_map(gemm_ctx* h, const void* ptr, int64_t rows, int64_t cols, int dtype,
-              int box_rows, CUtensorMap* out) {
+}  // namespace
+
+bool gb300::make_map(gemm_ctx* h, const void* ptr, int64_t rows, int64_t cols, int dtype,
+                     int box_rows, CUtensorMap* out) {
   const TmapKey key{ptr, rows, cols, dtype, box_rows};
   for (auto& e : h->cache)
     if (e.valid && e.key == key) {
@@ -136,6 +77,8 @@ bool make_map(gemm_ctx* h, const void* ptr, int64_t rows, int64_t cols, int dtyp
   *out = m;
   return true;
 }
+
+namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -556,6 +499,7 @@ const char* gemm_status_string(gemm_status_t s) {
     case GEMM_ERR_CUDA: return "CUDA error";
     case GEMM_ERR_OOM: return "out of memory";
     case GEMM_ERR_TIMEOUT: return "kernel wait timed out";
+    case GEMM_ERR_BAD_INDEX: return "index in device memory out of range";
     default: return "unknown status";
   }
 }
@@ -593,6 +537,7 @@ gemm_status_t gemm_destroy(gemm_handle_t h) {
   cudaFree(h->d_status);
   if (h->d_ws) cudaFree(h->d_ws);
   if (h->d_ctr) cudaFree(h->d_ctr);
+  if (h->d_op) cudaFree(h->d_op);
   for (auto* p : h->d_stage)
     if (p) cudaFree(p);
   if (h->copy_in) cudaStreamDestroy(h->copy_in);
@@ -1099,7 +1044,7 @@ gemm_status_t gemm_device_status(gemm_handle_t h, gemm_stream_t stream_, uint32_
   cudaMemset(h->d_status, 0, sizeof(uint32_t));
   if (h->d_ctr) cudaMemset(h->d_ctr, 0, h->ctr_count * sizeof(uint32_t));
   if (cudaDeviceSynchronize() != cudaSuccess) return GEMM_ERR_CUDA;
-  return GEMM_ERR_TIMEOUT;
+  return (word >> 24) == kDevBadIndex ? GEMM_ERR_BAD_INDEX : GEMM_ERR_TIMEOUT;
 }
 
 gemm_status_t gemm_run_host(gemm_handle_t h, const void* A_host, const void* B_host, void* C_host,

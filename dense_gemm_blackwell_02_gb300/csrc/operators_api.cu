@@ -1,0 +1,211 @@
+// C ABI of the operators around the projections (declared in include/gemm.h):
+// gemm_run_adapters, gemm_rotary and gemm_adjust_logits.  Argument validation,
+// workspace and launches; the kernels are in adapters_kernel.cu, rotary_kernel.cu and
+// logits_kernel.cu.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "context.h"
+#include "gemm.h"
+#include "operators.h"
+
+using namespace gb300;
+
+namespace {
+
+bool valid_dtype(int d) { return d >= GEMM_F16 && d <= GEMM_E5M2; }
+bool is_fp8(int d) { return d == GEMM_E4M3 || d == GEMM_E5M2; }
+int64_t elem_size(int d) { return d == GEMM_F32 ? 4 : 2; }
+bool aligned(const void* p, uint64_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// The handle's scratch for these operators, grown on demand.
+gemm_status_t ensure_scratch(gemm_ctx* h, size_t bytes) {
+  if (bytes <= h->op_bytes) return GEMM_OK;
+  if (h->d_op) cudaFree(h->d_op);
+  h->d_op = nullptr;
+  h->op_bytes = 0;
+  if (cudaMalloc(&h->d_op, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_OOM;
+  }
+  h->op_bytes = bytes;
+  return GEMM_OK;
+}
+
+gemm_status_t launched(gemm_ctx* h, cudaError_t e) {
+  h->last_cuda = e;
+  if (e == cudaSuccess) return GEMM_OK;
+  cudaGetLastError();
+  return GEMM_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, void* Y, int64_t M,
+                                int64_t N, int64_t K, gemm_dtype_t dtype_in,
+                                gemm_dtype_t dtype_out, const gemm_adapters_t* ad,
+                                const int32_t* row_adapter, gemm_stream_t stream_) {
+  if (!h || !ad) return GEMM_ERR_INVALID_ARG;
+  if (M < 0 || N < 0 || K < 0 || ad->count < 0 || ad->rank < 1) return GEMM_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype_in) || !valid_dtype(dtype_out)) return GEMM_ERR_INVALID_ARG;
+  if (dtype_in == GEMM_F32 || is_fp8(dtype_in) || is_fp8(dtype_out)) return GEMM_ERR_UNSUPPORTED;
+  if (ad->rank % 8 || ad->rank > kMaxRank) return GEMM_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return GEMM_OK;
+  if (!row_adapter || !Y || (K > 0 && (!X || !W))) return GEMM_ERR_INVALID_ARG;
+  if (ad->count > 0 && K > 0 && (!ad->down || !ad->up)) return GEMM_ERR_INVALID_ARG;
+  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+  if (!aligned(row_adapter, 4) || !aligned(Y, (uint64_t)elem_size(dtype_out))) return GEMM_ERR_UNSUPPORTED;
+  if (K == 0 || ad->count == 0)  // nothing to add: the product itself
+    return gemm_run(h, X, W, Y, M, N, K, dtype_in, dtype_out, stream_);
+  if (K % 8 || !aligned(X, 16) || !aligned(W, 16) || !aligned(ad->down, 16) ||
+      !aligned(ad->up, 16) || !aligned(ad->scale, 4))
+    return GEMM_ERR_UNSUPPORTED;
+  if ((int64_t)ad->count * ad->rank > INT32_MAX || (int64_t)ad->count * N > INT32_MAX)
+    return GEMM_ERR_UNSUPPORTED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+
+  // Scratch: u of every row, then (unless Y is binary32 itself) the shared product.
+  const size_t u_bytes = ((size_t)M * ad->rank * sizeof(float) + 255) & ~(size_t)255;
+  const size_t base_bytes = dtype_out == GEMM_F32 ? 0 : (size_t)M * N * sizeof(float);
+  gemm_status_t st = ensure_scratch(h, u_bytes + base_bytes);
+  if (st != GEMM_OK) return st;
+  char* scratch = static_cast<char*>(h->d_op);
+  void* base = dtype_out == GEMM_F32 ? Y : scratch + u_bytes;
+
+  AdapterParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.X = X;
+  p.down = ad->down;
+  p.up = ad->up;
+  p.scale = ad->scale;
+  p.row_adapter = row_adapter;
+  p.M = (int32_t)M;
+  p.N = (int32_t)N;
+  p.K = (int32_t)K;
+  p.rank = ad->rank;
+  p.count = ad->count;
+  p.U = reinterpret_cast<float*>(scratch);
+  p.base = static_cast<const float*>(base);
+  p.Y = Y;
+  p.status = h->d_status;
+  st = launched(h, launch_adapter_down(p, dtype_in, h->sms, stream));
+  if (st != GEMM_OK) return st;
+  st = gemm_run(h, X, W, base, M, N, K, dtype_in, GEMM_F32, stream_);
+  if (st != GEMM_OK) return st;
+  return launched(h, launch_adapter_up(p, dtype_in, dtype_out, h->sms, stream));
+}
+
+gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t tokens, int64_t heads,
+                          int64_t dim, int64_t x_token_stride, int64_t x_head_stride,
+                          int64_t y_token_stride, int64_t y_head_stride, gemm_dtype_t dtype,
+                          const gemm_rotary_t* r, gemm_stream_t stream_) {
+  if (!h || !r) return GEMM_ERR_INVALID_ARG;
+  if (tokens < 0 || heads < 0 || dim < 0 || x_token_stride < 0 || x_head_stride < 0 ||
+      y_token_stride < 0 || y_head_stride < 0)
+    return GEMM_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype)) return GEMM_ERR_INVALID_ARG;
+  if (is_fp8(dtype)) return GEMM_ERR_UNSUPPORTED;
+  if (tokens == 0 || heads == 0 || dim == 0) return GEMM_OK;
+  if (r->axes < 1 || r->axes > 8 || r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > dim ||
+      r->rot_dim > 2 * kMaxPairs || r->num_positions < 1 ||
+      (r->pairs != GEMM_PAIRS_HALF && r->pairs != GEMM_PAIRS_NEIGHBOURS) ||
+      (r->inverse != 0 && r->inverse != 1))
+    return GEMM_ERR_INVALID_ARG;
+  if (!x || !y || !r->cos || !r->sin || !r->positions) return GEMM_ERR_INVALID_ARG;
+  if (x == y && (x_token_stride != y_token_stride || x_head_stride != y_head_stride))
+    return GEMM_ERR_INVALID_ARG;
+  const int half = r->rot_dim / 2;
+  if (r->pair_axis)
+    for (int i = 0; i < half; ++i)
+      if (r->pair_axis[i] >= r->axes) return GEMM_ERR_INVALID_ARG;
+  const int64_t esz = elem_size(dtype);
+  if (tokens > INT32_MAX || heads > INT32_MAX || dim > INT32_MAX || tokens > INT32_MAX / heads)
+    return GEMM_ERR_UNSUPPORTED;
+  if (!aligned(x, (uint64_t)esz) || !aligned(y, (uint64_t)esz) || !aligned(r->cos, 4) ||
+      !aligned(r->sin, 4) || !aligned(r->positions, 4))
+    return GEMM_ERR_UNSUPPORTED;
+
+  RotaryParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = x;
+  p.y = y;
+  p.x_token = x_token_stride;
+  p.x_head = x_head_stride;
+  p.y_token = y_token_stride;
+  p.y_head = y_head_stride;
+  p.tokens = (int32_t)tokens;
+  p.heads = (int32_t)heads;
+  p.dim = (int32_t)dim;
+  p.half = half;
+  p.inverse = r->inverse;
+  p.cos = r->cos;
+  p.sin = r->sin;
+  p.positions = r->positions;
+  p.num_positions = r->num_positions;
+  p.status = h->d_status;
+  if (r->pair_axis) std::memcpy(p.pair_axis, r->pair_axis, (size_t)half);
+  // Vectors of 16 bytes: every head starts on a boundary, and the halves (or the pairs'
+  // end) and the head's end fall on one.
+  const bool neigh = r->pairs == GEMM_PAIRS_NEIGHBOURS;
+  const int64_t v = rotary_vector(dtype);
+  const bool vec = aligned(x, 16) && aligned(y, 16) &&
+                   (x_token_stride | x_head_stride | y_token_stride | y_head_stride) % v == 0 &&
+                   (neigh ? 2 * half : half) % v == 0 && (dim - 2 * half) % v == 0;
+  return launched(h, launch_rotary(p, dtype, neigh, vec, h->sms, reinterpret_cast<cudaStream_t>(stream_)));
+}
+
+gemm_status_t gemm_adjust_logits(gemm_handle_t h, const void* logits, void* out, int64_t rows,
+                                 int64_t vocab, int64_t logits_stride, int64_t out_stride,
+                                 gemm_dtype_t dtype_in, gemm_dtype_t dtype_out,
+                                 const gemm_logits_t* a, gemm_stream_t stream_) {
+  if (!h || !a) return GEMM_ERR_INVALID_ARG;
+  if (rows < 0 || vocab < 0 || logits_stride < vocab || out_stride < vocab) return GEMM_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype_in) || !valid_dtype(dtype_out)) return GEMM_ERR_INVALID_ARG;
+  if (is_fp8(dtype_in) || is_fp8(dtype_out)) return GEMM_ERR_UNSUPPORTED;
+  if (rows == 0 || vocab == 0) return GEMM_OK;
+  if (!logits || !out) return GEMM_ERR_INVALID_ARG;
+  if (a->tokens && !a->token_start) return GEMM_ERR_INVALID_ARG;
+  if (a->bias_tokens && (!a->bias_values || !a->bias_start)) return GEMM_ERR_INVALID_ARG;
+  if (a->mask && (a->mask_stride < (vocab + 31) / 32 || a->mask_count < 1 ||
+                  (!a->mask_row && a->mask_count < rows)))
+    return GEMM_ERR_INVALID_ARG;
+  if (logits == out && (dtype_in != dtype_out || logits_stride != out_stride)) return GEMM_ERR_INVALID_ARG;
+  if (vocab > (int64_t(1) << 30) || rows > (int64_t(1) << 24)) return GEMM_ERR_UNSUPPORTED;
+  if (rows * (vocab / 8192 + 2) > INT32_MAX) return GEMM_ERR_UNSUPPORTED;  // the grid
+  if (!aligned(logits, (uint64_t)elem_size(dtype_in)) || !aligned(out, (uint64_t)elem_size(dtype_out)) ||
+      !aligned(a->tokens, 4) || !aligned(a->token_start, 8) || !aligned(a->prompt_len, 4) ||
+      !aligned(a->repetition, 4) || !aligned(a->frequency, 4) || !aligned(a->presence, 4) ||
+      !aligned(a->bias_tokens, 4) || !aligned(a->bias_values, 4) || !aligned(a->bias_start, 8) ||
+      !aligned(a->mask, 4) || !aligned(a->mask_row, 4))
+    return GEMM_ERR_UNSUPPORTED;
+  LogitsParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.in = logits;
+  p.out = out;
+  p.in_stride = logits_stride;
+  p.out_stride = out_stride;
+  p.rows = (int32_t)rows;
+  p.vocab = (int32_t)vocab;
+  p.tokens = a->tokens;
+  p.token_start = a->token_start;
+  p.prompt_len = a->prompt_len;
+  p.repetition = a->repetition;
+  p.frequency = a->frequency;
+  p.presence = a->presence;
+  p.bias_tokens = a->bias_tokens;
+  p.bias_values = a->bias_values;
+  p.bias_start = a->bias_start;
+  p.mask = a->mask;
+  p.mask_stride = a->mask_stride;
+  p.mask_count = a->mask_count;
+  p.mask_row = a->mask_row;
+  p.status = h->d_status;
+  return launched(h, launch_logits(p, dtype_in, dtype_out, h->sms, reinterpret_cast<cudaStream_t>(stream_)));
+}
+
+}  // extern "C"

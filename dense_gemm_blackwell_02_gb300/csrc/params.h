@@ -22,7 +22,15 @@ constexpr int kChainKBlocks = 64;
 enum OutKind : int { kOutF16 = 0, kOutBF16 = 1, kOutF32 = 2 };
 
 // Device status word: 0 = fine; otherwise (code << 24) | (site << 16) | blockIdx.x.
-enum DeviceCode : uint32_t { kDevTimeout = 1u };
+enum DeviceCode : uint32_t {
+  kDevTimeout = 1u,   // a wait ran out (site: WaitSite)
+  kDevBadIndex = 2u,  // an index in device memory was out of range (site: IndexSite)
+};
+enum IndexSite : uint32_t {
+  kSiteRowAdapter = 1,  // row_adapter[i] >= count
+  kSitePosition = 2,    // a rotary position outside the tables
+  kSiteMaskRow = 3,     // mask_row[i] >= mask_count
+};
 enum WaitSite : uint32_t {
   kSiteEmpty = 1,     // producer waiting for a free stage
   kSiteFull = 2,      // MMA issuer waiting for a loaded stage
@@ -32,6 +40,9 @@ enum WaitSite : uint32_t {
   kSiteDrain = 6,     // teardown: outstanding copies / MMAs
   kSiteKx = 7,        // two-slice exchange through distributed shared memory
   kSiteClc = 8,       // cluster launch control: a free answer slot, or the next answer
+  kSiteAdapterFull = 9,   // adapters: MMA issuer waiting for a loaded stage
+  kSiteAdapterEmpty = 10, // adapters: producer waiting for a free stage
+  kSiteAdapterAcc = 11,   // adapters: epilogue waiting for the finished accumulator
 };
 
 // One problem of a grouped launch ("CUTLASS Deep Dive: From CuTe Layouts to Blackwell

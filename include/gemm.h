@@ -60,7 +60,9 @@ typedef enum {
                                not 16-byte aligned, no sm_103 device */
   GEMM_ERR_CUDA = 3,        /* a CUDA runtime / driver call failed */
   GEMM_ERR_OOM = 4,         /* device or host allocation failed */
-  GEMM_ERR_TIMEOUT = 5      /* a kernel wait exceeded its limit (see gemm_device_status) */
+  GEMM_ERR_TIMEOUT = 5,     /* a kernel wait exceeded its limit (see gemm_device_status) */
+  GEMM_ERR_BAD_INDEX = 6    /* an index in device memory was out of range (see
+                               gemm_device_status) */
 } gemm_status_t;
 
 /*
@@ -351,8 +353,11 @@ gemm_status_t gemm_plan(const gemm_device_model_t* dev, const gemm_config_t* for
 
 /* Synchronise `stream`, read and clear the handle's device status word.
  * Returns GEMM_ERR_TIMEOUT if a kernel gave up waiting since the last call
- * (the output of that run is undefined), else GEMM_OK.  *detail, if non-NULL,
- * receives the raw word (code << 24 | wait site << 16 | block index). */
+ * (the output of that run is undefined), GEMM_ERR_BAD_INDEX if a kernel of
+ * gemm_run_adapters, gemm_rotary or gemm_adjust_logits met an index out of its
+ * range (which it did not follow: see there), else GEMM_OK; of several only the
+ * first.  *detail, if non-NULL, receives the raw word (code << 24 | site << 16 |
+ * block index). */
 gemm_status_t gemm_device_status(gemm_handle_t h, gemm_stream_t stream, uint32_t* detail);
 
 /* Upper bound, in nanoseconds, on any single wait inside the kernels (default
@@ -412,6 +417,152 @@ const char* gemm_last_cuda_error(gemm_handle_t h);
 gemm_status_t gemm_run_noalloc(const void* A, const void* B, void* C, int64_t M, int64_t N,
                                int64_t K, gemm_dtype_t dtype_in, gemm_dtype_t dtype_out,
                                gemm_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Operators around the projections of a served language model.  Like gemm_run they are
+ * asynchronous on `stream`, use the handle's workspace (grown on the first call that
+ * needs more of it) and report argument errors before anything is queued.
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * A projection with low-rank adapters, a different one for every row:
+ *     Y[i] = W . X[i]  +  s[a] * Up[a] . (Down[a] . X[i]),      a = row_adapter[i]
+ * X: M x K, W: N x K, Y: M x N as A, B and C of gemm_run.  The rows of many requests
+ * share W; each request's rows name its adapter, in any order.  A negative
+ * row_adapter[i] means no adapter: Y[i] = W . X[i].
+ *   down      count x rank x K: adapter a's row r at down + (a * rank + r) * K elements
+ *   up        count x N x rank: adapter a's row n at up + (a * N + n) * rank elements
+ *   scale     count binary32 factors, or NULL for all 1
+ *   count     adapters in the pool, >= 0 (0, or no adapters: exactly gemm_run)
+ *   rank      a multiple of 8, 8..128; adapters of a lower rank are padded with zeros
+ * down and up hold dtype_in, 16-byte aligned; all of it is device memory of the caller.
+ * row_adapter: M values in device memory, so that a captured graph serves batches of
+ * any composition.  A value >= count is not followed (that row gets no adapter) and
+ * gemm_device_status reports GEMM_ERR_BAD_INDEX.
+ * An adapter's values reach only the rows that name it: infinities or NaN in one
+ * adapter leave the other rows as they are.
+ * Down . X and the sum of both terms are held in binary32.  Y is rounded once.
+ */
+typedef struct {
+  const void* down;
+  const void* up;
+  const float* scale;
+  int32_t count;
+  int32_t rank;
+} gemm_adapters_t;
+
+/* Errors as gemm_run, and:
+ *   GEMM_ERR_INVALID_ARG   adapters or row_adapter NULL (with M > 0), count < 0, rank < 1,
+ *                          down or up NULL with count > 0;
+ *   GEMM_ERR_UNSUPPORTED   FP8 inputs, rank not a multiple of 8 or above 128, down or up
+ *                          not 16-byte aligned, scale or row_adapter not 4-byte aligned,
+ *                          count * rank or count * N above INT32_MAX.
+ * K == 0 writes Y = 0.  gemm_set_config applies to the shared product. */
+gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, void* Y, int64_t M,
+                                int64_t N, int64_t K, gemm_dtype_t dtype_in,
+                                gemm_dtype_t dtype_out, const gemm_adapters_t* adapters,
+                                const int32_t* row_adapter, gemm_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height, width): in every head of every token
+ * the pair (a, b) number i turns by the angle whose cosine and sine stand in row
+ * positions[pair_axis[i]][token] of the tables, column i:
+ *     a' = a cos - b sin,     b' = b cos + a sin
+ *   x, y      tokens x heads x dim; element (t, h, d) of x at
+ *             x + t * x_token_stride + h * x_head_stride + d elements, y likewise.  y may
+ *             be x with the same strides (in place); otherwise they do not overlap.  The
+ *             rotated heads may be the first of a fused projection's rows.
+ *   dtype     GEMM_F16, GEMM_BF16 or GEMM_F32, of x and y; computed in binary32 and
+ *             rounded once
+ *   rot_dim   even, 2..min(dim, 512): the first rot_dim values of a head are rot_dim / 2
+ *             pairs, the rest is copied
+ *   pairs     GEMM_PAIRS_HALF: pair i is (x[i], x[i + rot_dim / 2]);
+ *             GEMM_PAIRS_NEIGHBOURS: (x[2 i], x[2 i + 1])
+ *   inverse   1: turn back (sin negated), which is the gradient: dx from dy
+ *   cos, sin  num_positions x rot_dim / 2 binary32
+ *   positions axes x tokens int32, axis after axis
+ *   pair_axis HOST memory, rot_dim / 2 values below axes, read before the call returns;
+ *             NULL: axis 0 for all
+ * A position outside 0..num_positions - 1 leaves its pairs unturned, and
+ * gemm_device_status reports GEMM_ERR_BAD_INDEX.
+ */
+typedef enum { GEMM_PAIRS_HALF = 0, GEMM_PAIRS_NEIGHBOURS = 1 } gemm_pairs_t;
+typedef struct {
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  const uint8_t* pair_axis;
+  int64_t num_positions;
+  int32_t axes;    /* 1..8 */
+  int32_t rot_dim;
+  int32_t pairs;   /* gemm_pairs_t */
+  int32_t inverse; /* 0 or 1 */
+} gemm_rotary_t;
+
+/* Errors: GEMM_ERR_INVALID_ARG for a NULL handle, rotary or (with work to do) pointer,
+ * negative sizes or strides, axes, rot_dim, pairs, inverse or a pair_axis out of range,
+ * num_positions < 1, or y == x with other strides; GEMM_ERR_UNSUPPORTED for an FP8 dtype,
+ * a pointer not aligned to its elements, or tokens * heads above INT32_MAX. */
+gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t tokens, int64_t heads,
+                          int64_t dim, int64_t x_token_stride, int64_t x_head_stride,
+                          int64_t y_token_stride, int64_t y_head_stride, gemm_dtype_t dtype,
+                          const gemm_rotary_t* rotary, gemm_stream_t stream);
+
+/*
+ * Logits before sampling: penalties for repeated tokens, biases, grammar masks.  For
+ * every row i and token v, in binary32 and in this order, rounded once to dtype_out:
+ *     z = logits[i][v]
+ *     if v is in row i's history:            z = z > 0 ? z / repetition[i] : z * repetition[i]
+ *     c times among its generated tokens:    z = z - frequency[i] * c - (c > 0 ? presence[i] : 0)
+ *     a bias w for v in row i's list:        z = z + w
+ *     masked out by row i's grammar:         z = -infinity, whatever it was
+ *   tokens, token_start, prompt_len
+ *             row i's history is tokens[token_start[i] .. token_start[i + 1] - 1]; its first
+ *             prompt_len[i] tokens are the prompt (prompt_len NULL: none), the rest was
+ *             generated.  Values outside 0..vocab - 1 are padding and count for nothing.
+ *             tokens NULL: no histories
+ *   repetition, frequency, presence
+ *             one binary32 value per row; NULL: 1, 0 and 0
+ *   bias_tokens, bias_values, bias_start
+ *             row i's biases are entries bias_start[i] .. bias_start[i + 1] - 1, in the
+ *             order of their tokens; several for one token add up, in that order.  Tokens
+ *             outside 0..vocab - 1 are ignored.  bias_tokens NULL: no biases
+ *   mask, mask_stride, mask_count, mask_row
+ *             mask_count bit masks of mask_stride 32-bit words (>= ceil(vocab / 32)); bit
+ *             v % 32 of word v / 32 set: token v may follow.  Row i uses mask mask_row[i]
+ *             (NULL: mask i); a negative one means no mask.  mask NULL: no masks.  A
+ *             mask_row >= mask_count is not followed (that row is not masked), and
+ *             gemm_device_status reports GEMM_ERR_BAD_INDEX
+ * logits and out are rows x vocab with row strides in elements; out may be logits with
+ * the same type and stride (in place), otherwise they do not overlap.  All pointers are
+ * device memory.  NaN stays NaN unless it is masked out.
+ */
+typedef struct {
+  const int32_t* tokens;
+  const int64_t* token_start;
+  const int32_t* prompt_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  const int64_t* bias_start;
+  const uint32_t* mask;
+  int64_t mask_stride;
+  int64_t mask_count;
+  const int32_t* mask_row;
+} gemm_logits_t;
+
+/* Errors: GEMM_ERR_INVALID_ARG for a NULL handle, adjust or (with work to do) pointer,
+ * negative sizes, a stride below vocab, tokens without token_start, bias_tokens without
+ * bias_values and bias_start, mask with mask_stride below ceil(vocab / 32) or mask_count
+ * < 1 (or, without mask_row, < rows), or out == logits with another type or stride;
+ * GEMM_ERR_UNSUPPORTED for an FP8 type, a pointer not aligned to its elements, vocab above
+ * 2^30 or rows above 2^24. */
+gemm_status_t gemm_adjust_logits(gemm_handle_t h, const void* logits, void* out, int64_t rows,
+                                 int64_t vocab, int64_t logits_stride, int64_t out_stride,
+                                 gemm_dtype_t dtype_in, gemm_dtype_t dtype_out,
+                                 const gemm_logits_t* adjust, gemm_stream_t stream);
 
 #ifdef __cplusplus
 }
