@@ -65,7 +65,7 @@ class GemmRotary(ctypes.Structure):
     """gemm_rotary_t: the tables, the tokens' positions along every axis, and which axis
     turns which pair."""
     _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
-                ("positions", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("pair_axis", ctypes.c_char_p),
                 ("num_positions", ctypes.c_int64), ("axes", ctypes.c_int32),
                 ("rot_dim", ctypes.c_int32), ("pairs", ctypes.c_int32),
                 ("inverse", ctypes.c_int32)]
@@ -180,25 +180,33 @@ def torch_float32():
     return torch.float32
 
 
-def torch_int32():
-    import torch
-    return torch.int32
+_torch = None        # torch, and its dtypes' codes: set when the first handle is made
+_DTYPE_CODE = None
+
+
+def _use_torch():
+    global _torch, _DTYPE_CODE
+    if _torch is None:
+        import torch
+        _torch = torch
+        _DTYPE_CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32,
+                       torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
 
 
 def torch_dtype_code(dt) -> int:
-    import torch
-    return {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32,
-            torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}[dt]
+    _use_torch()
+    return _DTYPE_CODE[dt]
 
 
-def _need(t, name, dtype, shape, device):
-    """Check an auxiliary tensor (None stays None) and give its address."""
+def _need(t, name, dtype, shape, index):
+    """Check an auxiliary tensor (None stays None) on CUDA device `index` and give its
+    address."""
     if t is None:
         return None
-    if (t.device != device or t.dtype != dtype or not t.is_contiguous()
-            or (shape is not None and tuple(t.shape) != tuple(shape))):
+    if (t.get_device() != index or t.dtype is not dtype or not t.is_contiguous()
+            or (shape is not None and t.shape != shape)):
         want = "" if shape is None else f" of shape {tuple(shape)}"
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor{want} on {device}")
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor{want} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -227,10 +235,19 @@ def _stream_ptr(stream, device):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_of(stream, index):
+    """_stream_ptr for a CUDA device given by its index, by the raw handle (a Stream object
+    around it costs 2 us of a 20 us call)."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 class Gemm:
     """One library handle (workspace, status word, tensor-map cache)."""
 
     def __init__(self):
+        _use_torch()
         h = ctypes.c_void_p()
         _check(lib().gemm_create(ctypes.byref(h)), "gemm_create")
         self._h = h
@@ -360,24 +377,25 @@ class Gemm:
         (no second term where a is negative): CUDA tensors X (M,K), W (N,K), Y (M,N), down
         (adapters, rank, K), up (adapters, N, rank) of X's dtype, row_adapter int32 (M),
         scale float32 (adapters) or None; all contiguous."""
-        if not (X.is_cuda and W.device == X.device and Y.device == X.device):
-            raise ValueError("X, W and Y must be CUDA tensors of one device")
+        if not X.is_cuda:
+            raise ValueError("X must be a CUDA tensor")
         if X.dim() != 2 or W.dim() != 2 or down.dim() != 3:
             raise ValueError("X and W must be 2-D, down and up 3-D")
         M, K = X.shape
         N = W.shape[0]
-        count, rank = down.shape[:2]
-        _need(X, "X", X.dtype, (M, K), X.device)
-        _need(W, "W", X.dtype, (N, K), X.device)
-        _need(Y, "Y", Y.dtype, (M, N), X.device)
-        ad = GemmAdapters(_need(down, "down", X.dtype, (count, rank, K), X.device),
-                          _need(up, "up", X.dtype, (count, N, rank), X.device),
-                          _need(scale, "scale", torch_float32(), (count,), X.device), count, rank)
-        rows = _need(row_adapter, "row_adapter", torch_int32(), (M,), X.device)
-        code = lib().gemm_run_adapters(self._h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), M, N, K,
-                                       torch_dtype_code(X.dtype), torch_dtype_code(Y.dtype),
-                                       ctypes.byref(ad), rows, _stream_ptr(stream, X.device))
-        _check(code, f"gemm_run_adapters M={M} N={N} K={K} rank={rank}", self._h)
+        count, rank, _ = down.shape
+        dev, dt = X.get_device(), X.dtype
+        ad = GemmAdapters(_need(down, "down", dt, (count, rank, K), dev),
+                          _need(up, "up", dt, (count, N, rank), dev),
+                          _need(scale, "scale", _torch.float32, (count,), dev), count, rank)
+        code = _lib.gemm_run_adapters(self._h, _need(X, "X", dt, (M, K), dev),
+                                      _need(W, "W", dt, (N, K), dev),
+                                      _need(Y, "Y", Y.dtype, (M, N), dev), M, N, K,
+                                      _DTYPE_CODE[dt], _DTYPE_CODE[Y.dtype], ctypes.byref(ad),
+                                      _need(row_adapter, "row_adapter", _torch.int32, (M,), dev),
+                                      _stream_of(stream, dev))
+        if code:
+            _check(code, f"gemm_run_adapters M={M} N={N} K={K} rank={rank}", self._h)
         return Y
 
     def rotary(self, x, y, cos, sin, positions, pair_axis=None, neighbours=False, inverse=False,
@@ -388,33 +406,36 @@ class Gemm:
         or (tokens,); pair_axis the axis of every pair (see pair_axes; None: the first).
         Pairs are (i, i + pairs), or neighbouring values.  inverse turns back (the
         gradient)."""
-        if not (x.is_cuda and y.device == x.device and y.dtype == x.dtype and x.dim() == 3
+        dev, dt = x.get_device(), x.dtype
+        if not (x.is_cuda and y.get_device() == dev and y.dtype is dt and x.dim() == 3
                 and y.shape == x.shape):
             raise ValueError("x and y must be CUDA tensors (tokens, heads, dim) of one device and dtype")
         T, H, D = x.shape
-        if D > 1 and (x.stride(2) != 1 or y.stride(2) != 1):
+        xt, xh, xd = x.stride()
+        yt, yh, yd = y.stride()
+        if D > 1 and (xd != 1 or yd != 1):
             raise ValueError("the values of a head must be contiguous")
         if positions.dim() == 1:
             positions = positions[None]
         if cos.dim() != 2 or positions.dim() != 2:
             raise ValueError("cos and sin must be (positions, pairs), positions (axes, tokens)")
-        half, axes = cos.shape[1], positions.shape[0]
-        axis_ptr = None
+        P, half = cos.shape
+        axes = positions.shape[0]
         if pair_axis is not None:
             if len(pair_axis) != half:
                 raise ValueError(f"pair_axis must name an axis for each of the {half} pairs")
-            if not all(0 <= a < axes for a in pair_axis):
+            pair_axis = bytes(pair_axis)
+            if half and max(pair_axis) >= axes:
                 raise ValueError(f"pair_axis must hold axes below {axes}")
-            axis_ptr = ctypes.cast((ctypes.c_uint8 * half)(*pair_axis), ctypes.c_void_p)
-        r = GemmRotary(_need(cos, "cos", torch_float32(), (cos.shape[0], half), x.device),
-                       _need(sin, "sin", torch_float32(), (cos.shape[0], half), x.device),
-                       _need(positions, "positions", torch_int32(), (axes, T), x.device),
-                       axis_ptr, cos.shape[0], axes, 2 * half,
-                       PAIRS_NEIGHBOURS if neighbours else PAIRS_HALF, 1 if inverse else 0)
-        code = lib().gemm_rotary(self._h, x.data_ptr(), y.data_ptr(), T, H, D, x.stride(0),
-                                 x.stride(1), y.stride(0), y.stride(1), torch_dtype_code(x.dtype),
-                                 ctypes.byref(r), _stream_ptr(stream, x.device))
-        _check(code, f"gemm_rotary tokens={T} heads={H} dim={D}", self._h)
+        f32 = _torch.float32
+        r = GemmRotary(_need(cos, "cos", f32, (P, half), dev), _need(sin, "sin", f32, (P, half), dev),
+                       _need(positions, "positions", _torch.int32, (axes, T), dev), pair_axis, P,
+                       axes, 2 * half, PAIRS_NEIGHBOURS if neighbours else PAIRS_HALF,
+                       1 if inverse else 0)
+        code = _lib.gemm_rotary(self._h, x.data_ptr(), y.data_ptr(), T, H, D, xt, xh, yt, yh,
+                                _DTYPE_CODE[dt], ctypes.byref(r), _stream_of(stream, dev))
+        if code:
+            _check(code, f"gemm_rotary tokens={T} heads={H} dim={D}", self._h)
         return y
 
     def adjust_logits(self, logits, out, tokens=None, token_start=None, prompt_len=None,
@@ -428,17 +449,25 @@ class Gemm:
         bias_start (int64, rows + 1) the biases; mask int32 (masks, words) with bit
         v % 32 of word v // 32 set where token v may follow, mask_row int32 (rows),
         negative for no mask, or None for one mask per row."""
-        import torch
-        if not (logits.is_cuda and out.device == logits.device and logits.dim() == 2
+        dev = logits.get_device()
+        if not (logits.is_cuda and out.get_device() == dev and logits.dim() == 2
                 and out.shape == logits.shape):
             raise ValueError("logits and out must be CUDA tensors (rows, vocab) of one device")
         B, V = logits.shape
-        if V > 1 and (logits.stride(1) != 1 or out.stride(1) != 1):
+        sl, cl = logits.stride()
+        so, co = out.stride()
+        if V > 1 and (cl != 1 or co != 1):
             raise ValueError("the logits of a row must be contiguous")
-        dev, f32, i32, i64 = logits.device, torch.float32, torch.int32, torch.int64
-        if mask is not None and mask.dim() != 2:
-            raise ValueError("mask must be (masks, words)")
-        nb = None if bias_tokens is None else bias_tokens.shape
+        if B > 1 and (sl < V or so < V):
+            raise ValueError("rows must not overlap")
+        if B == 1:  # a single row's stride says nothing
+            sl = so = V
+        f32, i32, i64 = _torch.float32, _torch.int32, _torch.int64
+        masks = words = 0
+        if mask is not None:
+            if mask.dim() != 2:
+                raise ValueError("mask must be (masks, words)")
+            masks, words = mask.shape
         a = GemmLogits(_need(tokens, "tokens", i32, None, dev),
                        _need(token_start, "token_start", i64, (B + 1,), dev),
                        _need(prompt_len, "prompt_len", i32, (B,), dev),
@@ -446,19 +475,16 @@ class Gemm:
                        _need(frequency, "frequency", f32, (B,), dev),
                        _need(presence, "presence", f32, (B,), dev),
                        _need(bias_tokens, "bias_tokens", i32, None, dev),
-                       _need(bias_values, "bias_values", f32, nb, dev),
+                       _need(bias_values, "bias_values", f32,
+                             None if bias_tokens is None else bias_tokens.shape, dev),
                        _need(bias_start, "bias_start", i64, (B + 1,), dev),
-                       _need(mask, "mask", i32, None, dev),
-                       0 if mask is None else mask.shape[1], 0 if mask is None else mask.shape[0],
+                       _need(mask, "mask", i32, None, dev), words, masks,
                        _need(mask_row, "mask_row", i32, (B,), dev))
-        # (a single row's or column's stride says nothing)
-        sl, so = (max(t.stride(0), V) if B > 1 else V for t in (logits, out))
-        if B > 1 and (logits.stride(0) < V or out.stride(0) < V):
-            raise ValueError("rows must not overlap")
-        code = lib().gemm_adjust_logits(self._h, logits.data_ptr(), out.data_ptr(), B, V, sl, so,
-                                        torch_dtype_code(logits.dtype), torch_dtype_code(out.dtype),
-                                        ctypes.byref(a), _stream_ptr(stream, dev))
-        _check(code, f"gemm_adjust_logits rows={B} vocab={V}", self._h)
+        code = _lib.gemm_adjust_logits(self._h, logits.data_ptr(), out.data_ptr(), B, V, sl, so,
+                                       _DTYPE_CODE[logits.dtype], _DTYPE_CODE[out.dtype],
+                                       ctypes.byref(a), _stream_of(stream, dev))
+        if code:
+            _check(code, f"gemm_adjust_logits rows={B} vocab={V}", self._h)
         return out
 
     def run_host(self, A, B, C, dtype_in, dtype_out, stream=None):

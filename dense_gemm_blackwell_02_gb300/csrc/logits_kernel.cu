@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kVec = 8;            // logits per thread and step
+constexpr int kTokens = 8;         // history tokens per thread in flight
 constexpr int kMaxSlice = 16384;   // words of table: 64 KiB, three CTAs per SM
 constexpr int kMinSlice = 2048;
 
@@ -86,13 +87,20 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
       if (p.presence) r.pres = p.presence[row];
       const int64_t t0 = p.token_start[row], t1 = p.token_start[row + 1];
       const int64_t said = t0 + (p.prompt_len ? p.prompt_len[row] : 0);
-      for (int64_t i = t0 + threadIdx.x; i < t1; i += kThreads) {
-        const int32_t v = p.tokens[i];
-        if (v < 0 || v >= p.vocab) continue;  // padding
-        const int32_t w = v + shift - w0;
-        if (w < 0 || w >= p.slice) continue;
-        if (i >= said) atomicAdd(table + w, 1u);
-        else atomicOr(table + w, kInPrompt);
+      for (int64_t i0 = t0; i0 < t1; i0 += kThreads * kTokens) {
+        int32_t v[kTokens];
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+          const int64_t i = i0 + j * kThreads + threadIdx.x;
+          v[j] = i < t1 ? __ldg(p.tokens + i) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+          const int32_t w = v[j] + shift - w0;
+          if (v[j] < 0 || v[j] >= p.vocab || w < 0 || w >= p.slice) continue;  // padding, or another slice's
+          if (i0 + j * kThreads + threadIdx.x >= said) atomicAdd(table + w, 1u);
+          else atomicOr(table + w, kInPrompt);
+        }
       }
     }
     if (p.bias_tokens) {

@@ -30,7 +30,7 @@ struct RotaryParams {
   const int32_t* positions;
   int64_t num_positions;
   uint32_t* status;
-  uint8_t pair_axis[kMaxPairs];
+  alignas(8) uint8_t pair_axis[kMaxPairs];
 };
 
 // vec: 16-byte accesses of x, y and the tables are aligned and no vector straddles the

@@ -21,6 +21,37 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxRun = 4;  // heads whose loads are in flight together
 
+// Whether one axis turns N pairs, whose bytes start at a multiple of N.
+template <int N>
+__device__ __forceinline__ bool one_axis(const uint8_t* axis) {
+  if constexpr (N == 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(axis);
+    return w.x == w.y && w.x == (w.x & 0xFFu) * 0x01010101u;
+  } else if constexpr (N == 4) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(axis);
+    return w == (w & 0xFFu) * 0x01010101u;
+  } else {
+    return N == 2 ? axis[0] == axis[1] : true;
+  }
+}
+
+// N values of a table's row (16-byte aligned for N >= 4, 8-byte for 2).
+template <int N>
+__device__ __forceinline__ void load_row(const float* p, float (&f)[N]) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + j));
+      f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+    f[0] = v.x, f[1] = v.y;
+  } else {
+    f[0] = __ldg(p);
+  }
+}
+
 // NEIGH: neighbouring pairs.  V: elements per vector (1: no alignment is assumed).
 template <typename T, bool NEIGH, int V>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
@@ -69,18 +100,34 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       }
     }
     float c[kPairs], s[kPairs];
-#pragma unroll
-    for (int j = 0; j < kPairs; ++j) {
-      const int64_t pos = p.positions[(int64_t)p.pair_axis[i0 + j] * p.tokens + t];
-      c[j] = 1.0f;
-      s[j] = 0.0f;
+    if (V > 1 && one_axis<kPairs>(p.pair_axis + i0)) {
+      // one position for the whole vector: its cosines and sines stand in a row
+      const int64_t pos = p.positions[(int64_t)p.pair_axis[i0] * p.tokens + t];
       if (pos >= 0 && pos < p.num_positions) {
-        c[j] = __ldg(p.cos + pos * p.half + i0 + j);
-        s[j] = __ldg(p.sin + pos * p.half + i0 + j);
-        if (p.inverse) s[j] = -s[j];
+        load_row<kPairs>(p.cos + pos * p.half + i0, c);
+        load_row<kPairs>(p.sin + pos * p.half + i0, s);
       } else {
         record_bad_index(p.status, kSitePosition);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) c[j] = 1.0f, s[j] = 0.0f;
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const int64_t pos = p.positions[(int64_t)p.pair_axis[i0 + j] * p.tokens + t];
+        c[j] = 1.0f;
+        s[j] = 0.0f;
+        if (pos >= 0 && pos < p.num_positions) {
+          c[j] = __ldg(p.cos + pos * p.half + i0 + j);
+          s[j] = __ldg(p.sin + pos * p.half + i0 + j);
+        } else {
+          record_bad_index(p.status, kSitePosition);
+        }
+      }
+    }
+    if (p.inverse) {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) s[j] = -s[j];
     }
 #pragma unroll
     for (int k = 0; k < kMaxRun; ++k) {
