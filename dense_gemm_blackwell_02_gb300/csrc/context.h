@@ -45,6 +45,8 @@ struct gemm_ctx {
   size_t stage_bytes[3] = {0, 0, 0};
   void* d_op = nullptr;  // scratch of the operators around the projections
   size_t op_bytes = 0;
+  uint32_t* d_op_ctr = nullptr;
+  size_t op_ctr_count = 0;
   gemm_config_t forced = {};
   gemm_config_t last = {};
   uint64_t wait_limit_ns = 2000000000ull;

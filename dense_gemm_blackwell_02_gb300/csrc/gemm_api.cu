@@ -538,6 +538,7 @@ gemm_status_t gemm_destroy(gemm_handle_t h) {
   if (h->d_ws) cudaFree(h->d_ws);
   if (h->d_ctr) cudaFree(h->d_ctr);
   if (h->d_op) cudaFree(h->d_op);
+  if (h->d_op_ctr) cudaFree(h->d_op_ctr);
   for (auto* p : h->d_stage)
     if (p) cudaFree(p);
   if (h->copy_in) cudaStreamDestroy(h->copy_in);
@@ -1040,9 +1041,10 @@ gemm_status_t gemm_device_status(gemm_handle_t h, gemm_stream_t stream_, uint32_
     return GEMM_ERR_CUDA;
   if (detail) *detail = word;
   if (word == 0) return GEMM_OK;
-  // An aborted split-K run may leave arrival counters behind: clear them too.
+  // An aborted split-K run (or slices of adapters) may leave arrival counters behind: clear them too.
   cudaMemset(h->d_status, 0, sizeof(uint32_t));
   if (h->d_ctr) cudaMemset(h->d_ctr, 0, h->ctr_count * sizeof(uint32_t));
+  if (h->d_op_ctr) cudaMemset(h->d_op_ctr, 0, h->op_ctr_count * sizeof(uint32_t));
   if (cudaDeviceSynchronize() != cudaSuccess) return GEMM_ERR_CUDA;
   return (word >> 24) == kDevBadIndex ? GEMM_ERR_BAD_INDEX : GEMM_ERR_TIMEOUT;
 }

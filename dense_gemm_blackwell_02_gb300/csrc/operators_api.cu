@@ -11,6 +11,7 @@
 #include "context.h"
 #include "gemm.h"
 #include "operators.h"
+#include "umma.cuh"
 
 using namespace gb300;
 
@@ -21,17 +22,33 @@ bool is_fp8(int d) { return d == GEMM_E4M3 || d == GEMM_E5M2; }
 int64_t elem_size(int d) { return d == GEMM_F32 ? 4 : 2; }
 bool aligned(const void* p, uint64_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// The handle's scratch for these operators, grown on demand.
-gemm_status_t ensure_scratch(gemm_ctx* h, size_t bytes) {
-  if (bytes <= h->op_bytes) return GEMM_OK;
-  if (h->d_op) cudaFree(h->d_op);
-  h->d_op = nullptr;
-  h->op_bytes = 0;
-  if (cudaMalloc(&h->d_op, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_OOM;
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// The handle's scratch for these operators, grown on demand; its counters are zero between
+// calls.
+gemm_status_t ensure_scratch(gemm_ctx* h, size_t bytes, size_t counters) {
+  if (bytes > h->op_bytes) {
+    if (h->d_op) cudaFree(h->d_op);
+    h->d_op = nullptr;
+    h->op_bytes = 0;
+    if (cudaMalloc(&h->d_op, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_ERR_OOM;
+    }
+    h->op_bytes = bytes;
   }
-  h->op_bytes = bytes;
+  if (counters > h->op_ctr_count) {
+    if (h->d_op_ctr) cudaFree(h->d_op_ctr);
+    h->d_op_ctr = nullptr;
+    h->op_ctr_count = 0;
+    if (cudaMalloc(&h->d_op_ctr, counters * sizeof(uint32_t)) != cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_ERR_OOM;
+    }
+    if (cudaMemset(h->d_op_ctr, 0, counters * sizeof(uint32_t)) != cudaSuccess) return GEMM_ERR_CUDA;
+    h->op_ctr_count = counters;
+  }
   return GEMM_OK;
 }
 
@@ -58,7 +75,8 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   if (M == 0 || N == 0) return GEMM_OK;
   if (!row_adapter || !Y || (K > 0 && (!X || !W))) return GEMM_ERR_INVALID_ARG;
   if (ad->count > 0 && K > 0 && (!ad->down || !ad->up)) return GEMM_ERR_INVALID_ARG;
-  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+  if (M > INT32_MAX - kAdapterRows || N > INT32_MAX - kAdapterCols || K > INT32_MAX)
+    return GEMM_ERR_UNSUPPORTED;
   if (!aligned(row_adapter, 4) || !aligned(Y, (uint64_t)elem_size(dtype_out))) return GEMM_ERR_UNSUPPORTED;
   if (K == 0 || ad->count == 0)  // nothing to add: the product itself
     return gemm_run(h, X, W, Y, M, N, K, dtype_in, dtype_out, stream_);
@@ -69,19 +87,8 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     return GEMM_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
-  // Scratch: u of every row, then (unless Y is binary32 itself) the shared product.
-  const size_t u_bytes = ((size_t)M * ad->rank * sizeof(float) + 255) & ~(size_t)255;
-  const size_t base_bytes = dtype_out == GEMM_F32 ? 0 : (size_t)M * N * sizeof(float);
-  gemm_status_t st = ensure_scratch(h, u_bytes + base_bytes);
-  if (st != GEMM_OK) return st;
-  char* scratch = static_cast<char*>(h->d_op);
-  void* base = dtype_out == GEMM_F32 ? Y : scratch + u_bytes;
-
   AdapterParams p;
   std::memset(&p, 0, sizeof(p));
-  p.X = X;
-  p.down = ad->down;
-  p.up = ad->up;
   p.scale = ad->scale;
   p.row_adapter = row_adapter;
   p.M = (int32_t)M;
@@ -89,15 +96,52 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   p.K = (int32_t)K;
   p.rank = ad->rank;
   p.count = ad->count;
-  p.U = reinterpret_cast<float*>(scratch);
-  p.base = static_cast<const float*>(base);
+  p.tiles = (int32_t)ceil_div(M, kAdapterRows);
+  p.k_blocks = (int32_t)ceil_div(K, kBlockK);
+  p.x_rows = (int32_t)std::min<int64_t>(M, kAdapterRows);
+  // Both kernels hold two CTAs per SM.  The CTAs of a row tile share its work, of which
+  // there is at most a K slice of four blocks for every group of adapters, and a column
+  // tile.
+  const int64_t ctas = std::max<int64_t>(1, (int64_t)2 * h->sms / p.tiles);
+  const int64_t per_group = kAdapterCols / p.rank;
+  const int64_t groups = ceil_div(std::min<int64_t>(p.x_rows, ad->count), per_group);
+  p.max_splits = (int32_t)std::min<int64_t>(std::max<int64_t>(1, p.k_blocks / 4), ctas);
+  p.down_ctas = (int32_t)std::min<int64_t>(ctas, groups * p.max_splits);
+  p.up_ctas = (int32_t)std::min<int64_t>(ctas, ceil_div(N, kAdapterCols));
+  p.vec_store = aligned(Y, 16) && (N * elem_size(dtype_out)) % 16 == 0;
+  p.idesc = idesc_f16_kmajor(kAdapterRows, 0, dtype_in == GEMM_BF16);
   p.Y = Y;
   p.status = h->d_status;
-  st = launched(h, launch_adapter_down(p, dtype_in, h->sms, stream));
+  p.wait_limit_ns = h->wait_limit_ns;
+  p.test_stall = h->test_stall;
+
+  // Scratch: u of every row, its K slices, and (unless Y holds it) the shared product.
+  const size_t u_bytes = round_up((size_t)M * p.rank * sizeof(float));
+  const size_t part_bytes =
+      round_up((size_t)p.tiles * p.max_splits * kAdapterRows * p.rank * sizeof(float));
+  const bool base_in_y = dtype_out == GEMM_F32;
+  const size_t base_bytes = base_in_y ? 0 : (size_t)M * N * sizeof(float);
+  gemm_status_t st = ensure_scratch(h, u_bytes + part_bytes + base_bytes, (size_t)p.tiles * kAdapterRows);
+  if (st != GEMM_OK) return st;
+  char* scratch = static_cast<char*>(h->d_op);
+  p.U = reinterpret_cast<float*>(scratch);
+  p.partial = reinterpret_cast<float*>(scratch + u_bytes);
+  p.counters = h->d_op_ctr;
+  void* base = base_in_y ? Y : scratch + u_bytes + part_bytes;
+
+  CUtensorMap tmX, tmDown, tmUp;
+  if (!make_map(h, X, M, K, dtype_in, p.x_rows, &tmX) ||
+      !make_map(h, ad->down, (int64_t)ad->count * p.rank, K, dtype_in, p.rank, &tmDown) ||
+      !make_map(h, ad->up, (int64_t)ad->count * N, p.rank, dtype_in, kAdapterCols, &tmUp))
+    return GEMM_ERR_CUDA;
+
+  st = launched(h, launch_adapter_down(tmX, tmDown, p, stream));
   if (st != GEMM_OK) return st;
   st = gemm_run(h, X, W, base, M, N, K, dtype_in, GEMM_F32, stream_);
   if (st != GEMM_OK) return st;
-  return launched(h, launch_adapter_up(p, dtype_in, dtype_out, h->sms, stream));
+  p.base = static_cast<const float*>(base);
+  p.vec_store = p.vec_store && N % 4 == 0;  // (base's rows too)
+  return launched(h, launch_adapter_up(tmUp, p, dtype_in, dtype_out, stream));
 }
 
 gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t tokens, int64_t heads,

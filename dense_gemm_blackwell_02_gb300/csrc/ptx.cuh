@@ -401,6 +401,27 @@ __device__ __forceinline__ void umma_commit_pair_elect(uint32_t bar, uint16_t ct
                : "memory");
 }
 
+// One MMA of 16 fp16/bf16 values of K (one CTA); `accumulate` 0 overwrites D.
+__device__ __forceinline__ void umma_f16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(GB300_ELECT
+               ".reg .pred p_;\n\tsetp.ne.b32 p_, %4, 0;\n\t"
+               "@e_ tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p_;\n\t}" ::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+
+// 32 lanes x 32 bits, 8 consecutive columns, waited for.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
 // 32 lanes x 32 bits, 32 consecutive columns: thread t of the warp receives lane
 // (quarter*32 + t), columns [col, col+32).
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
