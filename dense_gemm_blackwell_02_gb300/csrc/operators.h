@@ -71,6 +71,36 @@ constexpr int kMaxRank = 128;
 constexpr int kAdapterRows = 128;   // rows of X per tile
 constexpr int kAdapterCols = 128;   // columns: of Down . X per group of adapters, of Y per tile
 
+// A batch of few rows (adapters_few_kernel.cu), queued right after the shared product.
+constexpr int kFewRows = 512;
+constexpr int kFewGroup = 16;  // rows of one adapter that are taken together
+struct FewGroup {
+  int32_t adapter;          // -1: none
+  int32_t rows;             // how many
+  int32_t row[kFewGroup];   // -1 past them
+  int32_t pad[14];          // 128 bytes
+};
+struct AdapterFewParams {
+  const void* X;        // M x K, M <= kFewRows
+  const void* down;     // count x rank x K
+  const void* up;       // count x N x rank
+  const float* scale;   // count, or nullptr
+  const int32_t* row_adapter;
+  int32_t M, N, K, rank, count;
+  int32_t slices;       // partial sums of u (few_slices)
+  int32_t vec_store;    // 16-byte accesses of eight columns of Y are aligned
+  int32_t vec_base;     // rows of base start on 16 bytes
+  float* partial;       // M x slices x rank
+  FewGroup* groups;     // M
+  uint32_t* counts;     // groups listed, CTAs that have read that; zero between calls
+  const float* base;    // M x N: W . x; may be Y
+  void* Y;              // M x N
+  uint32_t* status;
+};
+int few_slices(int32_t M, int32_t K, int32_t rank, int32_t count, int sms);
+cudaError_t launch_adapter_few(const AdapterFewParams& p, int elem_in, int elem_out, int sms,
+                               cudaStream_t stream);
+
 struct AdapterParams {
   const float* scale;   // count, or nullptr
   const int32_t* row_adapter;

@@ -87,6 +87,41 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     return GEMM_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
+  const bool base_in_y = dtype_out == GEMM_F32;
+  if (M <= kFewRows) {
+    AdapterFewParams f;
+    std::memset(&f, 0, sizeof(f));
+    f.slices = few_slices((int32_t)M, (int32_t)K, ad->rank, ad->count, h->sms);
+    const size_t base_bytes = base_in_y ? 0 : round_up((size_t)M * N * sizeof(float));
+    const size_t part_bytes = round_up((size_t)M * f.slices * ad->rank * sizeof(float));
+    gemm_status_t st = ensure_scratch(
+        h, base_bytes + part_bytes + (size_t)M * sizeof(FewGroup), 2);
+    if (st != GEMM_OK) return st;
+    char* scratch = static_cast<char*>(h->d_op);
+    void* base = base_in_y ? Y : scratch;
+    st = gemm_run(h, X, W, base, M, N, K, dtype_in, GEMM_F32, stream_);
+    if (st != GEMM_OK) return st;
+    f.X = X;
+    f.down = ad->down;
+    f.up = ad->up;
+    f.scale = ad->scale;
+    f.row_adapter = row_adapter;
+    f.M = (int32_t)M;
+    f.N = (int32_t)N;
+    f.K = (int32_t)K;
+    f.rank = ad->rank;
+    f.count = ad->count;
+    f.vec_store = aligned(Y, 16) && N % 8 == 0;
+    f.vec_base = aligned(base, 16) && N % 4 == 0;
+    f.partial = reinterpret_cast<float*>(scratch + base_bytes);
+    f.groups = reinterpret_cast<FewGroup*>(scratch + base_bytes + part_bytes);
+    f.counts = h->d_op_ctr;
+    f.base = static_cast<const float*>(base);
+    f.Y = Y;
+    f.status = h->d_status;
+    return launched(h, launch_adapter_few(f, dtype_in, dtype_out, h->sms, stream));
+  }
+
   AdapterParams p;
   std::memset(&p, 0, sizeof(p));
   p.scale = ad->scale;
@@ -119,7 +154,6 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   const size_t u_bytes = round_up((size_t)M * p.rank * sizeof(float));
   const size_t part_bytes =
       round_up((size_t)p.tiles * p.max_splits * kAdapterRows * p.rank * sizeof(float));
-  const bool base_in_y = dtype_out == GEMM_F32;
   const size_t base_bytes = base_in_y ? 0 : (size_t)M * N * sizeof(float);
   gemm_status_t st = ensure_scratch(h, u_bytes + part_bytes + base_bytes, (size_t)p.tiles * kAdapterRows);
   if (st != GEMM_OK) return st;
