@@ -1,15 +1,19 @@
 // Low-rank adapters beside a shared projection, a different one for every row:
 //     Y[i] = W . X[i] + s * Up[a] . (Down[a] . X[i]),   a = row_adapter[i]
-// W . X is the GEMM's.  Two kernels add the rest:
-//     u[i] = s * Down[a] . X[i]          (adapter_down_kernel, binary32)
-//     Y[i] = base[i] + Up[a] . u[i]      (adapter_up_kernel, rounded once)
+// for many rows.  The kernel here forms u[i] = s * Down[a] . X[i] in binary32; the GEMM then
+// appends Up[a] . u[i] to every tile (ADAPT in gemm_kernel.cuh), so that Y is written once,
+// rounded once, and nothing of its size is read or written besides.
 //
-// Both work on tiles of 128 rows in their own order, whatever adapters they name.  A tile's
+// The rows are taken 128 at a time in their own order, whatever adapters they name.  A tile's
 // distinct adapters are numbered (slots), and the tensor cores multiply the whole tile by
 // each of them, every adapter into accumulator columns of its own; a row then takes the
 // columns of the one it names.  So rows need no sorting, nothing of one adapter enters
 // another row's sums (infinities and NaN included), and the surplus products cost nothing
-// that is scarce: the adapters' weights, read once per tile, bound both kernels.
+// that is scarce: X, read once (134 MB at 8192 x 8192, 20 us of HBM), bounds the kernel.
+//
+// u leaves as two 16-bit parts, u = 2^e (hi + lo) with e the exponent of the row's largest
+// value: fp16's range cannot cut it off, and at least 17 of its bits reach the second product
+// (one part alone would round u to 8 or 11 bits, an error of the size of Y's own rounding).
 #include <algorithm>
 
 #include "elements.cuh"
@@ -114,50 +118,117 @@ __device__ void number_slots(TileSlots& ts, const AdapterParams& p, int32_t row0
   __syncthreads();
 }
 
-// Among the four warps that take results out: a barrier, and one that tells whether
-// `fail` held in any thread (so that they leave a loop with barriers together).
-__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool epilogue_any(bool fail) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p_, q_;\n\tsetp.ne.u32 p_, %1, 0;\n\t"
-      "bar.red.or.pred q_, 1, 128, p_;\n\tselp.u32 %0, 1, 0, q_;\n\t}"
-      : "=r"(any)
-      : "r"(fail ? 1u : 0u)
-      : "memory");
-  return any != 0;
-}
-
 // Where a CTA's barriers stand in shared memory.
 struct Bars {
   uint32_t base;
   __device__ uint32_t full(uint32_t s) const { return base + 8u * s; }
   __device__ uint32_t empty(uint32_t s) const { return base + 8u * (kMaxStages + s); }
-  __device__ uint32_t acc_full(uint32_t i) const { return base + 8u * (2 * kMaxStages + i); }
-  __device__ uint32_t acc_empty(uint32_t i) const { return base + 8u * (2 * kMaxStages + 2 + i); }
-  __device__ uint32_t drain() const { return base + 8u * (2 * kMaxStages + 4); }
+  __device__ uint32_t acc_full() const { return base + 8u * (2 * kMaxStages); }
+  __device__ uint32_t acc_empty() const { return base + 8u * (2 * kMaxStages + 1); }
+  __device__ uint32_t drain() const { return base + 8u * (2 * kMaxStages + 2); }
   __device__ void init() const {
     for (uint32_t s = 0; s < kMaxStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (uint32_t i = 0; i < 2; ++i) {
-      mbar_init(acc_full(i), 1);
-      mbar_init(acc_empty(i), 4);
-    }
+    mbar_init(acc_full(), 1);
+    mbar_init(acc_empty(), 4);
     mbar_init(drain(), 1);
     fence_mbarrier_init();
   }
 };
-constexpr int kNumBars = 2 * kMaxStages + 5;
+constexpr int kNumBars = 2 * kMaxStages + 3;
 
 // ---------------------------------------------------------------------------- Down . X --
-// The CTAs of a row tile share its (group of adapters, K slice) units: as many K slices as
-// leave every CTA one unit.  A group is what fits 128 accumulator columns.  Slices meet in
-// global memory: the last of a group to arrive adds them in slice order.
-constexpr uint32_t kDownRing = 96 * 1024;  // two CTAs per SM
-constexpr uint32_t kDownSmem = kDownRing + 1024;
+// A row tile belongs to a cluster of CTAs, which share its (group of adapters, K slice)
+// units: as many K slices as leave every CTA one unit.  A group is what fits 128 accumulator
+// columns.  The slices meet in distributed shared memory (the idle operand ring), where each
+// CTA of a group adds its share of the rows, in slice order.
+constexpr uint32_t kRing = 96 * 1024;  // two CTAs per SM
+constexpr uint32_t kSmem = kRing + 1024;
 
+// u = 2^e (hi + lo) of `n` values of a row whose largest magnitude is `big`: the factor that
+// brings it near 1 and its inverse; 1 for zero, infinities and NaN (which pass through).
+__device__ __forceinline__ void row_factors(float big, float& inv, float& back) {
+  int32_t e = (int32_t)(__float_as_uint(big) >> 23);
+  if (e == 0 || e == 255) e = 127;
+  e = min(max(e, 2), 252);
+  inv = __uint_as_float((uint32_t)(254 - e) << 23);
+  back = __uint_as_float((uint32_t)e << 23);
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_parts(T* hi, T* lo, const float (&v)[N], float inv) {
+  struct alignas(N * sizeof(T)) { T x[N]; } h, l;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float x = v[k] * inv;
+    h.x[k] = from_f32<T>(x);
+    const float f = to_f32(h.x[k]);
+    l.x[k] = from_f32<T>(isinf(f) ? 0.0f : x - f);
+  }
+  *reinterpret_cast<decltype(h)*>(hi) = h;
+  *reinterpret_cast<decltype(l)*>(lo) = l;
+}
+
+// The adapters of two row tiles, as the GEMM's 256-row tile takes them.
+__device__ void list_tile(const AdapterParams& p, int32_t pair, TileSlots& t0, TileSlots& t1) {
+  number_slots(t0, p, 2 * pair * kAdapterRows);
+  number_slots(t1, p, (2 * pair + 1) * kAdapterRows);
+  AdapterTile& out = p.pairs[pair];
+  const int t = (int)threadIdx.x;
+  const int warp = (int)warp_id(), lane = (int)lane_id();
+  __shared__ int16_t place[kAdapterRows];  // of the second tile's slots in the list
+  __shared__ int16_t twin[kAdapterRows];   // the second tile's slot of a first one's adapter
+  if (t < kAdapterRows) {
+    twin[t] = -1;
+    place[t] = -1;
+  }
+  __syncthreads();
+  for (int s = t; s < t1.slots; s += kThreads)
+    for (int q = 0; q < t0.slots; ++q)
+      if (t0.adapter[q] == t1.adapter[s]) place[s] = (int16_t)q, twin[q] = (int16_t)s;
+  __syncthreads();
+  if (t == 0) {
+    int n = t0.slots;
+    for (int s = 0; s < t1.slots; ++s)
+      if (place[s] < 0) place[s] = (int16_t)n++;
+    out.slots = n;
+  }
+  __syncthreads();
+  if (warp < 4) {
+    const int r = warp * 32 + lane, s0 = t0.slot[r], s1 = t1.slot[r];
+    for (int q = 0; q < t0.slots; ++q) {
+      const uint32_t m0 = __ballot_sync(0xFFFFFFFFu, s0 == q);
+      const uint32_t m1 = __ballot_sync(0xFFFFFFFFu, twin[q] >= 0 && s1 == twin[q]);
+      if (lane == 0) {
+        out.slot[q].adapter = t0.adapter[q];
+        out.slot[q].disable[warp] = ~m0;
+        out.slot[q].disable[4 + warp] = ~m1;
+      }
+    }
+    for (int q = 0; q < t1.slots; ++q) {
+      if (place[q] < t0.slots) continue;
+      const uint32_t m1 = __ballot_sync(0xFFFFFFFFu, s1 == q);
+      if (lane == 0) {
+        out.slot[place[q]].adapter = t1.adapter[q];
+        out.slot[place[q]].disable[warp] = 0xFFFFFFFFu;
+        out.slot[place[q]].disable[4 + warp] = ~m1;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
     adapter_down_kernel(const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmDown, const AdapterParams p) {
@@ -166,11 +237,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ alignas(8) uint64_t bar_mem[kNumBars];
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t abort_mem;
-  __shared__ int32_t last_mem;
   const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const Bars bars{smem_addr(bar_mem)};
   const uint32_t warp = warp_id(), lane = lane_id();
   const WaitCtl ctl{p.wait_limit_ns, p.status, &abort_mem};
+  const int32_t tile = (int32_t)blockIdx.x / p.ctas;
+  const int32_t cta = (int32_t)blockIdx.x - tile * p.ctas;  // rank in the cluster
+
+  if (tile >= p.tiles) {  // the clusters after the row tiles' list the adapters of pairs of them
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int32_t pair = (int32_t)blockIdx.x - p.tiles * p.ctas;
+    if (2 * pair < p.tiles)
+      list_tile(p, pair, ts, *reinterpret_cast<TileSlots*>(smem_raw));
+    return;
+  }
 
   if (warp == 0 && lane == 0) {
     bars.init();
@@ -189,25 +270,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  const int32_t tile = (int32_t)blockIdx.x / p.down_ctas;
-  const int32_t cta = (int32_t)blockIdx.x - tile * p.down_ctas;
   number_slots(ts, p, tile * kAdapterRows);
   const int32_t per_group = kAdapterCols / p.rank;
   const int32_t groups = (ts.slots + per_group - 1) / per_group;
-  const int32_t splits = groups == 0 ? 1 : min(max(p.down_ctas / groups, 1), p.max_splits);
+  const int32_t splits = groups == 0 ? 1 : min(max(p.ctas / groups, 1), p.max_splits);
   const int32_t units = groups * splits;
-  // A stage: X's rows, then the group's rows of Down; the MMA's N is a multiple of 16, and
-  // it reads 128 rows of X (those past the box only feed rows that nobody takes).
-  const uint32_t x_bytes = ((uint32_t)p.x_rows * kRowBytes + 1023u) & ~1023u;
+  // A stage: X's rows, then the group's rows of Down; the MMA's N is a multiple of 16.
   const uint32_t n_max = ((uint32_t)(min(per_group, ts.slots) * p.rank) + 15u) & ~15u;
-  const uint32_t stage_bytes = x_bytes + n_max * kRowBytes;
-  const uint32_t reach = max(stage_bytes, kTileBytes);
-  const uint32_t stages = min((uint32_t)kMaxStages, 1u + (kDownRing - reach) / max(stage_bytes, 1u));
+  const uint32_t stage_bytes = kTileBytes + n_max * kRowBytes;
+  const uint32_t stages = min((uint32_t)kMaxStages, kRing / stage_bytes);
+  const int32_t pitch = 2 * kBlockK * (p.rank <= kBlockK ? 1 : 2);  // of U's rows
+  T* U = static_cast<T*>(p.U) + (int64_t)tile * kAdapterRows * pitch;
+  // value c of a row: 64 at a time, their high parts before their low parts
+  auto place_of = [](int32_t c) { return (c >> 6) * 2 * kBlockK + (c & (kBlockK - 1)); };
+  if (cta == 0 && threadIdx.x < kAdapterRows && ts.slot[threadIdx.x] < 0 &&
+      tile * kAdapterRows + (int32_t)threadIdx.x < p.M)
+    p.row_scale[tile * kAdapterRows + (int32_t)threadIdx.x] = 0.0f;
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
     bool ok = true;
-    for (int32_t u = cta; ok && u < units; u += p.down_ctas) {
+    for (int32_t u = cta; ok && u < units; u += p.ctas) {
       const int32_t group = u / splits, s = u - group * splits;
       const int32_t g0 = group * per_group, n = min(per_group, ts.slots - g0);
       const int32_t kb1 = (int32_t)((int64_t)(s + 1) * p.k_blocks / splits);
@@ -217,11 +300,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         const uint32_t at = ring + stage * stage_bytes;
-        mbar_arrive_expect_tx_elect(bars.full(stage), (uint32_t)(p.x_rows + n * p.rank) * kRowBytes);
-        for (int32_t j = 0; j < n; ++j)
-          tma_load_2d_elect(at + x_bytes + (uint32_t)(j * p.rank) * kRowBytes, &tmDown, kb * kBlockK,
-                            ts.adapter[g0 + j] * p.rank, bars.full(stage));
+        mbar_arrive_expect_tx_elect(bars.full(stage), (uint32_t)(kAdapterRows + n * p.rank) * kRowBytes);
         tma_load_2d_elect(at, &tmX, kb * kBlockK, tile * kAdapterRows, bars.full(stage));
+        for (int32_t j = 0; j < n; ++j)
+          tma_load_2d_elect(at + kTileBytes + (uint32_t)(j * p.rank) * kRowBytes, &tmDown, kb * kBlockK,
+                            ts.adapter[g0 + j] * p.rank, bars.full(stage));
         armed |= 1u << stage;
         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
         if (++stage == stages) stage = 0, phase ^= 1u;
@@ -235,11 +318,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp == 1) {
     uint32_t stage = 0, phase = 0, iter = 0;
     bool ok = !p.test_stall || warp_wait(bars.drain(), 0, ctl, kSiteTestStall);
-    for (int32_t u = cta; ok && u < units; u += p.down_ctas, ++iter) {
+    for (int32_t u = cta; ok && u < units; u += p.ctas, ++iter) {
       const int32_t group = u / splits, s = u - group * splits;
       const int32_t n = min(per_group, ts.slots - group * per_group);
       const uint32_t idesc = p.idesc | ((((uint32_t)(n * p.rank) + 15u) >> 4) << 18);  // N >> 3 at bit 17
-      if (!warp_wait_inl(bars.acc_empty(0), (iter & 1u) ^ 1u, ctl, kSiteAdapterAcc)) break;
+      if (!warp_wait_inl(bars.acc_empty(), (iter & 1u) ^ 1u, ctl, kSiteAdapterAcc)) break;
       tc_fence_after();
       const int32_t kb0 = (int32_t)((int64_t)s * p.k_blocks / splits);
       const int32_t kb1 = (int32_t)((int64_t)(s + 1) * p.k_blocks / splits);
@@ -250,13 +333,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         tc_fence_after();
         const uint32_t at = ring + stage * stage_bytes;
-        umma_stage_elect<1>(tmem, smem_desc_sw128_kmajor(at), smem_desc_sw128_kmajor(at + x_bytes),
+        umma_stage_elect<1>(tmem, smem_desc_sw128_kmajor(at), smem_desc_sw128_kmajor(at + kTileBytes),
                             idesc, kb > kb0 ? 1u : 0u, bars.empty(stage));
         if (++stage == stages) stage = 0, phase ^= 1u;
       }
-      if (ok) umma_commit_elect<1>(bars.acc_full(0));
+      if (ok) umma_commit_elect<1>(bars.acc_full());
     }
-    // every MMA has read its operands and written its columns before the CTA tears down
+    // every MMA has read its operands and written its columns before the ring is reused and
+    // the CTA tears down
     umma_commit_elect<1>(bars.drain());
     if (lane == 0) wait_parity_drain(bars.drain(), 0, ctl);
     __syncwarp();
@@ -264,351 +348,145 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t quarter = warp & 3u;
     const int32_t row = (int32_t)(quarter * 32 + lane);
     const int32_t slot = ts.slot[row];
-    const int32_t quads = p.rank / 4;
     uint32_t iter = 0;
-    for (int32_t u = cta; u < units; u += p.down_ctas, ++iter) {
-      const int32_t group = u / splits, s = u - group * splits;
-      const int32_t g0 = group * per_group, n = min(per_group, ts.slots - g0);
-      if (epilogue_any(!warp_wait_inl(bars.acc_full(0), iter & 1u, ctl, kSiteAdapterAcc))) break;
+    for (int32_t u = cta; u < units; u += p.ctas, ++iter) {
+      const int32_t g0 = u / splits * per_group, n = min(per_group, ts.slots - g0);
+      if (!warp_wait_inl(bars.acc_full(), iter & 1u, ctl, kSiteAdapterAcc)) break;
       tc_fence_after();
-      float* dst = splits == 1
-                       ? p.U + (int64_t)(tile * kAdapterRows + row) * p.rank
-                       : p.partial + ((int64_t)(tile * p.max_splits + s) * kAdapterRows + row) * p.rank;
-      const float f = splits == 1 && slot >= 0 && p.scale ? p.scale[ts.adapter[slot]] : 1.0f;
+      const float f = slot >= 0 && p.scale ? p.scale[ts.adapter[slot]] : 1.0f;
       for (int32_t j = 0; j < n; ++j) {
         const bool mine = slot == g0 + j;
         if (!__any_sync(0xFFFFFFFFu, mine)) continue;
-        for (int32_t c = 0; c < p.rank; c += 8) {
-          uint32_t v[8];
-          tmem_ld_32x32b_x8(tmem + ((quarter * 32u) << 16) + (uint32_t)(j * p.rank + c), v);
-          if (mine) {
+        const uint32_t at = tmem + ((quarter * 32u) << 16) + (uint32_t)(j * p.rank);
+        if (splits > 1) {
+          // a partial sum: into the ring, rows of rank + 4 values (on different banks)
+          const uint32_t dst = ring + (uint32_t)(row * (p.rank + 4)) * 4u;
+          for (int32_t c = 0; c < p.rank; c += 8) {
+            uint32_t v[8];
+            tmem_ld_32x32b_x8(at + (uint32_t)c, v);
+            if (mine) {
+              st_shared_v4(dst + 4u * (uint32_t)c, v[0], v[1], v[2], v[3]);
+              st_shared_v4(dst + 4u * (uint32_t)c + 16u, v[4], v[5], v[6], v[7]);
+            }
+          }
+        } else {
+          // the whole sum: its largest value, then its parts
+          float big = 0.0f, inv, back;
+          for (int32_t c = 0; c < p.rank; c += 8) {
+            uint32_t v[8];
+            tmem_ld_32x32b_x8(at + (uint32_t)c, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f * __uint_as_float(v[k])));
+          }
+          row_factors(big, inv, back);
+          if (mine) p.row_scale[tile * kAdapterRows + row] = back;
+          // (eight zeros past a rank that is not a multiple of the MMA's 16)
+          for (int32_t c = 0; c < ((p.rank + 15) & ~15); c += 8) {
+            uint32_t v[8] = {};
+            if (c < p.rank) tmem_ld_32x32b_x8(at + (uint32_t)c, v);
             float o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = f * __uint_as_float(v[k]);
-            store_f32<float, 8>(dst + c, o);
+            T* dst = U + (int64_t)row * pitch + place_of(c);
+            if (mine) store_parts<T, 8>(dst, dst + kBlockK, o, inv);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars.acc_empty(0));
-      if (splits == 1) continue;
-      // hand the slice over; the last one to arrive adds them all, in order
-      __threadfence();
-      epilogue_barrier();
-      if (threadIdx.x == 64) {
-        uint32_t* ctr = p.counters + tile * kAdapterRows + group;
-        const uint32_t old = atom_add_acq_rel_gpu(ctr, 1u);
-        last_mem = old == (uint32_t)splits - 1u;
-        if (last_mem) st_relaxed_gpu_u32(ctr, 0u);
-      }
-      epilogue_barrier();
-      if (last_mem) {
-        __threadfence();
-        const int32_t r0 = ts.start[g0], count = (ts.start[g0 + n] - r0) * quads;
-        const float* part = p.partial + (int64_t)tile * p.max_splits * kAdapterRows * p.rank;
-        const int64_t pitch = (int64_t)kAdapterRows * p.rank;
-        for (int32_t i = (int32_t)threadIdx.x - 64; i < count; i += 128) {
-          const int32_t r = ts.order[r0 + i / quads], c = (i % quads) * 4;
-          const float* src = part + (int64_t)r * p.rank + c;
-          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int32_t k = 0; k < splits; k += 8) {
-            uint4 v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              v[q] = k + q < splits ? ld_global_cg_v4(src + (k + q) * pitch) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (k + q < splits) {
-                sum.x += __uint_as_float(v[q].x);
-                sum.y += __uint_as_float(v[q].y);
-                sum.z += __uint_as_float(v[q].z);
-                sum.w += __uint_as_float(v[q].w);
-              }
-          }
-          const float f2 = p.scale ? p.scale[ts.id[r]] : 1.0f;
-          *reinterpret_cast<float4*>(p.U + (int64_t)(tile * kAdapterRows + r) * p.rank + c) =
-              make_float4(f2 * sum.x, f2 * sum.y, f2 * sum.z, f2 * sum.w);
-        }
-      }
-      epilogue_barrier();  // last_mem may change
+      if (lane == 0) mbar_arrive(bars.acc_empty());
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (splits > 1) {  // the same for the whole cluster: every CTA has one unit or none
+    cluster_sync();
+    if (cta < units && threadIdx.x < 128) {
+      // this CTA's rows of its group, four threads to a row
+      const int32_t group = cta / splits, s = cta - group * splits;
+      const int32_t r0 = ts.start[group * per_group];
+      const int32_t r1 = ts.start[min((group + 1) * per_group, ts.slots)];
+      const int32_t quad = (int32_t)threadIdx.x & 3;
+      const int32_t rounds = (r1 - r0 + 32 * splits - 1) / (32 * splits);
+      for (int32_t k = 0; k < rounds; ++k) {
+        const int32_t i = r0 + (k * 32 + ((int32_t)threadIdx.x >> 2)) * splits + s;
+        const bool on = i < r1;
+        const int32_t row = ts.order[min(i, r1 - 1)];
+        const float f = p.scale ? p.scale[ts.id[row]] : 1.0f;
+        const uint32_t src = ring + (uint32_t)(row * (p.rank + 4)) * 4u;
+        constexpr int kQuads = kMaxRank / 16;  // of four values, per thread
+        float v[kQuads][4];
+        float big = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+          const int32_t c = (q * 4 + quad) * 4;
+          v[q][0] = v[q][1] = v[q][2] = v[q][3] = 0.0f;
+          if (q * 16 >= p.rank) break;
+          if (c < p.rank) {
+            for (int32_t j = 0; j < splits; ++j) {
+              const float4 x = ld_cluster_v4(mapa_shared(src + 4u * (uint32_t)c, (uint32_t)(group * splits + j)));
+              v[q][0] += x.x, v[q][1] += x.y, v[q][2] += x.z, v[q][3] += x.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[q][e] *= f;
+              big = fmaxf(big, fabsf(v[q][e]));
+            }
+          }
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+        float inv, back;
+        row_factors(big, inv, back);
+        if (on && quad == 0) p.row_scale[tile * kAdapterRows + row] = back;
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+          const int32_t c = (q * 4 + quad) * 4;
+          T* dst = U + (int64_t)row * pitch + place_of(c);
+          if (on && c < ((p.rank + 15) & ~15)) store_parts<T, 4>(dst, dst + kBlockK, v[q], inv);
+        }
+      }
+    }
+    cluster_sync();  // the others have read this CTA's sums
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, kAdapterCols);
   }
 }
 
-// ------------------------------------------------------------------------------ Up . u --
-// The CTAs of a row tile share Y's column tiles.  The tile's u is the row operand of every
-// product: it is split into two 16-bit parts, u = 2^e (hi + lo) with e the exponent of the
-// row's largest value, so that fp16's range cannot cut it off and at least 17 of its bits
-// reach the product (one part alone would round u to 8 or 11 bits, an error of the size of
-// Y's own rounding).  A column tile times a slot's adapter lands in one of two accumulators.
-constexpr uint32_t kUpRing2 = 4;  // stages with ranks up to 64; 2 above
-
-__host__ __device__ constexpr uint32_t up_stages(int rank) { return rank <= 64 ? kUpRing2 : 2; }
-__host__ __device__ constexpr uint32_t up_smem(int rank) {
-  return (rank <= 64 ? 2u : 4u) * kTileBytes + up_stages(rank) * kTileBytes + 1024u;
-}
-
-template <typename T, typename TO, bool BASE>
-__global__ void __launch_bounds__(kThreads, 2)
-    adapter_up_kernel(const __grid_constant__ CUtensorMap tmUp, const AdapterParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ TileSlots ts;
-  __shared__ alignas(8) uint64_t bar_mem[kNumBars];
-  __shared__ float row_scale[kAdapterRows];
-  __shared__ uint32_t tmem_slot;
-  __shared__ int32_t abort_mem;
-  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const int32_t chunks = p.rank <= 64 ? 1 : 2;
-  const uint32_t ring = base + 2u * (uint32_t)chunks * kTileBytes;
-  const uint32_t stages = up_stages(p.rank);
-  const Bars bars{smem_addr(bar_mem)};
-  const uint32_t warp = warp_id(), lane = lane_id();
-  const WaitCtl ctl{p.wait_limit_ns, p.status, &abort_mem};
-
-  if (warp == 0 && lane == 0) {
-    bars.init();
-    abort_mem = 0;
-    tma_prefetch_desc(&tmUp);
-  }
-  if (warp == 1) {
-    tmem_alloc<1>(smem_addr(&tmem_slot), 2 * kAdapterCols);
-    tmem_relinquish<1>();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  grid_dependency_wait();
-  grid_launch_dependents();
-
-  const int32_t tile = (int32_t)blockIdx.x / p.up_ctas;
-  const int32_t cta = (int32_t)blockIdx.x - tile * p.up_ctas;
-  const int32_t n_tiles = (p.N + kAdapterCols - 1) / kAdapterCols;
-  number_slots(ts, p, tile * kAdapterRows);
-
-  // u -> the row operand: part (2 * chunk + lo) is a 128 x 64 tile in the 128-byte swizzle
-  if (threadIdx.x < kAdapterRows) {
-    const int32_t row = (int32_t)threadIdx.x;
-    const bool any = ts.slot[row] >= 0;
-    const float* u = p.U + (int64_t)(tile * kAdapterRows + row) * p.rank;
-    float big = 0.0f;
-    if (any)
-      for (int32_t c = 0; c < p.rank; c += 8) {
-        float v[8];
-        load_f32<float, 8>(u + c, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(v[k]));
-      }
-    // 2^e and its inverse from the exponent field; 1 for zero and for infinities (NaN is
-    // not counted by fmaxf and passes through any scaling)
-    int32_t e = (int32_t)(__float_as_uint(big) >> 23);
-    if (e == 0 || e == 255) e = 127;
-    e = min(max(e, 2), 252);
-    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-    row_scale[row] = __uint_as_float((uint32_t)e << 23);
-    for (int32_t c = 0; c < 64 * chunks; c += 8) {
-      Pack<T, 8> hi, lo;
-      float v[8] = {};
-      if (any && c < p.rank) load_f32<float, 8>(u + c, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float x = v[k] * inv;
-        hi.v[k] = from_f32<T>(x);
-        const float h = to_f32(hi.v[k]);
-        lo.v[k] = from_f32<T>(isinf(h) ? 0.0f : x - h);
-      }
-      const uint32_t at = base + (uint32_t)(c >> 6) * 2u * kTileBytes + (uint32_t)row * kRowBytes +
-                          ((((uint32_t)c >> 3) & 7u) ^ ((uint32_t)row & 7u)) * 16u;
-      const uint4 h4 = *reinterpret_cast<const uint4*>(&hi), l4 = *reinterpret_cast<const uint4*>(&lo);
-      st_shared_v4(at, h4.x, h4.y, h4.z, h4.w);
-      st_shared_v4(at + kTileBytes, l4.x, l4.y, l4.z, l4.w);
-    }
-    fence_proxy_async_smem();
-  }
-  __syncthreads();
-
-  if (warp == 0) {
-    uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
-    bool ok = true;
-    for (int32_t j = cta; ok && j < n_tiles; j += p.up_ctas)
-      for (int32_t d = 0; ok && d < ts.slots; ++d)
-        for (int32_t c = 0; c < chunks; ++c) {
-          if (!warp_wait_inl(bars.empty(stage), phase ^ 1u, ctl, kSiteAdapterEmpty)) {
-            ok = false;
-            break;
-          }
-          // (the last tile's rows past N are the next adapter's: columns that are not stored)
-          mbar_arrive_expect_tx_elect(bars.full(stage), kTileBytes);
-          tma_load_2d_elect(ring + stage * kTileBytes, &tmUp, c * kBlockK,
-                            ts.adapter[d] * p.N + j * kAdapterCols, bars.full(stage));
-          armed |= 1u << stage;
-          armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == stages) stage = 0, phase ^= 1u;
-        }
-    if (lane == 0)
-      for (uint32_t s = 0; s < stages; ++s)
-        if (armed & (1u << s)) wait_parity_drain(bars.full(s), (armed_phase >> s) & 1u, ctl);
-    __syncwarp();
-  } else if (warp == 1) {
-    uint32_t stage = 0, phase = 0, iter = 0;
-    bool ok = true;
-    const uint32_t idesc = p.idesc | ((uint32_t)(kAdapterCols >> 3) << 17);
-    for (int32_t j = cta; ok && j < n_tiles; j += p.up_ctas)
-      for (int32_t d = 0; ok && d < ts.slots; ++d, ++iter) {
-        const uint32_t slot = iter & 1u;
-        if (!warp_wait_inl(bars.acc_empty(slot), ((iter >> 1) & 1u) ^ 1u, ctl, kSiteAdapterAcc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int32_t c = 0; c < chunks; ++c) {
-          if (!warp_wait_inl(bars.full(stage), phase, ctl, kSiteAdapterFull)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t b = smem_desc_sw128_kmajor(ring + stage * kTileBytes);
-          const int32_t steps = (min(p.rank - 64 * c, 64) + 15) / 16;
-          for (int32_t part = 0; part < 2; ++part) {
-            const uint64_t a = smem_desc_sw128_kmajor(base + (uint32_t)(2 * c + part) * kTileBytes);
-            for (int32_t k = 0; k < steps; ++k)  // 16 values: 32 bytes, 2 in the descriptor
-              umma_f16_elect(tmem + slot * kAdapterCols, a + 2u * (uint32_t)k, b + 2u * (uint32_t)k,
-                             idesc, (c | part | k) ? 1u : 0u);
-          }
-          umma_commit_elect<1>(bars.empty(stage));
-          if (++stage == stages) stage = 0, phase ^= 1u;
-        }
-        if (ok) umma_commit_elect<1>(bars.acc_full(slot));
-      }
-    umma_commit_elect<1>(bars.drain());
-    if (lane == 0) wait_parity_drain(bars.drain(), 0, ctl);
-    __syncwarp();
-  } else {
-    const uint32_t quarter = warp & 3u;
-    const int32_t row = (int32_t)(quarter * 32 + lane);
-    const int64_t i = (int64_t)tile * kAdapterRows + row;
-    const int32_t slot = ts.slot[row];
-    const bool live = i < p.M;
-    const float rs = row_scale[row];
-    uint32_t iter = 0;
-    // one piece of 32 columns of this thread's row: base + rs * v
-    auto write = [&](int32_t n0, const uint32_t (&v)[32]) {
-      TO* y = static_cast<TO*>(p.Y) + i * p.N + n0;
-      const float* b = BASE ? p.base + i * p.N + n0 : nullptr;
-      constexpr int V = 16 / (int)sizeof(TO);
-      if (p.vec_store && n0 + 32 <= p.N) {
-#pragma unroll
-        for (int c = 0; c < 32; c += V) {
-          float o[V];
-          if constexpr (BASE) {
-            load_f32<float, V>(b + c, o);
-          } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) o[k] = 0.0f;
-          }
-#pragma unroll
-          for (int k = 0; k < V; ++k) o[k] = fmaf(rs, __uint_as_float(v[c + k]), o[k]);
-          store_f32<TO, V>(y + c, o);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (n0 + c < p.N) y[c] = from_f32<TO>(fmaf(rs, __uint_as_float(v[c]), BASE ? b[c] : 0.0f));
-      }
-    };
-    bool ok = true;
-    for (int32_t j = cta; ok && j < n_tiles; j += p.up_ctas) {
-      const int32_t n0 = j * kAdapterCols;
-      // rows without an adapter: the base alone (in place already there), or zero
-      if (live && slot < 0 && !(BASE && static_cast<const void*>(p.base) == p.Y)) {
-        const uint32_t zero[32] = {};
-        for (int32_t c = 0; c < kAdapterCols; c += 32) write(n0 + c, zero);
-      }
-      for (int32_t d = 0; d < ts.slots; ++d, ++iter) {
-        const uint32_t acc = iter & 1u;
-        if (!warp_wait_inl(bars.acc_full(acc), (iter >> 1) & 1u, ctl, kSiteAdapterAcc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const bool mine = live && slot == d;
-        if (__any_sync(0xFFFFFFFFu, mine)) {
-          for (int32_t c = 0; c < kAdapterCols; c += 32) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(tmem + ((quarter * 32u) << 16) + acc * kAdapterCols + (uint32_t)c, v);
-            tmem_ld_wait(v);
-            if (mine) write(n0 + c, v);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.acc_empty(acc));
-      }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc<1>(tmem, 2 * kAdapterCols);
-  }
-}
-
-template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), int64_t grid, uint32_t smem, cudaStream_t stream,
-                   const Args&... args) {
+template <typename T>
+cudaError_t launch(const CUtensorMap& tmX, const CUtensorMap& tmDown, const AdapterParams& p,
+                   cudaStream_t stream) {
+  auto kernel = adapter_down_kernel<T>;
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
+  const int64_t pairs = ((int64_t)p.tiles + 1) / 2;
+  const int64_t clusters = p.tiles + (pairs + p.ctas - 1) / p.ctas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.gridDim = dim3((unsigned)(clusters * p.ctas), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <typename T, typename TO>
-cudaError_t up_by_base(const CUtensorMap& tmUp, const AdapterParams& p, cudaStream_t stream) {
-  const int64_t grid = (int64_t)p.tiles * p.up_ctas;
-  return p.base ? launch(adapter_up_kernel<T, TO, true>, grid, up_smem(p.rank), stream, tmUp, p)
-                : launch(adapter_up_kernel<T, TO, false>, grid, up_smem(p.rank), stream, tmUp, p);
-}
-
-template <typename T>
-cudaError_t up_by_out(const CUtensorMap& tmUp, const AdapterParams& p, int elem_out,
-                      cudaStream_t stream) {
-  switch (elem_out) {
-    case kElemF16: return up_by_base<T, __half>(tmUp, p, stream);
-    case kElemBF16: return up_by_base<T, __nv_bfloat16>(tmUp, p, stream);
-    case kElemF32: return up_by_base<T, float>(tmUp, p, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, tmX, tmDown, p);
 }
 
 }  // namespace
 
 cudaError_t launch_adapter_down(const CUtensorMap& tmX, const CUtensorMap& tmDown,
-                                const AdapterParams& p, cudaStream_t stream) {
-  return launch(adapter_down_kernel, (int64_t)p.tiles * p.down_ctas, kDownSmem, stream, tmX, tmDown, p);
-}
-
-cudaError_t launch_adapter_up(const CUtensorMap& tmUp, const AdapterParams& p, int elem_in,
-                              int elem_out, cudaStream_t stream) {
-  if (elem_in == kElemF16) return up_by_out<__half>(tmUp, p, elem_out, stream);
-  return up_by_out<__nv_bfloat16>(tmUp, p, elem_out, stream);
+                                const AdapterParams& p, int elem_in, cudaStream_t stream) {
+  return elem_in == kElemF16 ? launch<__half>(tmX, tmDown, p, stream)
+                             : launch<__nv_bfloat16>(tmX, tmDown, p, stream);
 }
 
 }  // namespace gb300

@@ -6,6 +6,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <functional>
 
 #include "gemm.h"
 #include "params.h"
@@ -81,5 +82,13 @@ namespace gb300 {
 // K tails); stores skip them.
 bool make_map(gemm_ctx* h, const void* ptr, int64_t rows, int64_t cols, int dtype, int box_rows,
               CUtensorMap* out);
+
+// The product of a CTA-pair kernel with low-rank adapters appended to its tiles.  `before`
+// queues the kernel that prepares what `ad` points to, once the configuration is known to
+// serve the shape.
+gemm_status_t run_adapted(gemm_ctx* h, const void* A, const void* B, void* C, int64_t M, int64_t N,
+                          int64_t K, gemm_dtype_t dtype_in, gemm_dtype_t dtype_out,
+                          const AdaptParams<true>& ad, const std::function<cudaError_t()>& before,
+                          gemm_stream_t stream);
 
 }  // namespace gb300

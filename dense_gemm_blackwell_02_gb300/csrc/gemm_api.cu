@@ -605,7 +605,8 @@ namespace {
 gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, int64_t M,
                        int64_t N, int64_t K, gemm_dtype_t dtype_in, gemm_dtype_t dtype_out,
                        const gemm_epilogue_t* epi, const gemm_block_scales_t* bs,
-                       gemm_stream_t stream_) {
+                       gemm_stream_t stream_, const AdaptParams<true>* ad = nullptr,
+                       const std::function<cudaError_t()>* before = nullptr) {
   if (!h) return GEMM_ERR_INVALID_ARG;
   if (bs) {
     if (!bs->sfa || !bs->sfb || bs->block_m < 1) return GEMM_ERR_INVALID_ARG;
@@ -644,8 +645,8 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
   const gemm_config_t& fc = h->forced;
   if (fc.variant == 3 || (!fc.variant && !fc.block_n && !fc.splits && !fc.stages && !fc.epilogue &&
                           !fc.chain_kblocks && fc.swap_ab != 2 && M == 1 && K <= kGemvAutoMaxK &&
-                          !fused && !fp8_in && !bs)) {
-    if (M > kGemvMaxRows || fused || fp8_in || bs) return GEMM_ERR_UNSUPPORTED;
+                          !fused && !fp8_in && !bs && !ad)) {
+    if (M > kGemvMaxRows || fused || fp8_in || bs || ad) return GEMM_ERR_UNSUPPORTED;
     GemvSpec g;
     g.A = A;
     g.B = B;
@@ -666,12 +667,29 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
   if (fc.scheduler == 2) return GEMM_ERR_UNSUPPORTED;  // (cluster launch control: grouped launches)
   Choice ch;
   const bool fp8 = is_fp8(dtype_in);
-  gemm_status_t st = choose(h, M, N, K, out, fp8 ? 2 * kBlockK : kBlockK, bs != nullptr,
-                            !fp8 && !fused && !bs, &ch);
+  gemm_status_t st;
+  if (ad) {
+    // one kernel serves it: CTA pairs, 256 columns, the general epilogue
+    const gemm_config_t asked = h->forced;
+    if ((asked.variant && asked.variant != 2) || (asked.block_n && asked.block_n != 256) ||
+        asked.epilogue > 1 || asked.swap_ab == 2)
+      return GEMM_ERR_UNSUPPORTED;
+    h->forced.variant = 2;
+    h->forced.block_n = 256;
+    h->forced.epilogue = 1;
+    st = choose(h, M, N, K, out, kBlockK, false, false, &ch);
+    h->forced = asked;
+  } else {
+    st = choose(h, M, N, K, out, fp8 ? 2 * kBlockK : kBlockK, bs != nullptr, !fp8 && !fused && !bs, &ch);
+  }
   if (st != GEMM_OK) return st;
 
   LaunchSpec s;
   std::memset(&s, 0, sizeof(s));
+  if (ad) {
+    s.adapt = true;
+    s.ad = *ad;
+  }
   s.cta_group = ch.variant;
   s.bn = ch.bn;
   s.stages = ch.stages;
@@ -683,7 +701,7 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
   // FP8 kernels always carry the epilogue: the per-tensor scales arrive as alpha
   s.fused = (fused || fp8) && !bs;
   s.kind = bs ? 2 : fp8 ? 1 : 0;
-  s.staged = !ch.kx2 && !ch.swap && !s.fused && s.kind == 0 && !ch.one_chain &&
+  s.staged = !ch.kx2 && !ch.swap && !s.fused && !ad && s.kind == 0 && !ch.one_chain &&
              ((ch.splits > 1 && !ch.half_tail) || ch.sk_workers);
   s.stream = stream;
   const bool c_tma = reinterpret_cast<uintptr_t>(C) % 16 == 0 && ((size_t)N * osz) % 16 == 0;
@@ -773,6 +791,7 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
     p.workspace = h->d_ws;
     p.counters = h->d_ctr;
   }
+  if (before && (h->last_cuda = (*before)()) != cudaSuccess) return GEMM_ERR_CUDA;
   if ((h->last_cuda = launch_gemm(s)) != cudaSuccess) return GEMM_ERR_CUDA;
   h->last = gemm_config_t{ch.variant,  ch.bn,   ch.sk_workers ? -(int32_t)ch.sk_workers : ch.splits,
                           ch.stages,
@@ -1146,3 +1165,10 @@ gemm_status_t gemm_run_host(gemm_handle_t h, const void* A_host, const void* B_h
 }
 
 }  // extern "C"
+
+gemm_status_t gb300::run_adapted(gemm_ctx* h, const void* A, const void* B, void* C, int64_t M,
+                                 int64_t N, int64_t K, gemm_dtype_t dtype_in,
+                                 gemm_dtype_t dtype_out, const AdaptParams<true>& ad,
+                                 const std::function<cudaError_t()>& before, gemm_stream_t stream) {
+  return run_impl(h, A, B, C, M, N, K, dtype_in, dtype_out, nullptr, nullptr, stream, &ad, &before);
+}

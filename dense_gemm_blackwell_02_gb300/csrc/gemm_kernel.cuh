@@ -612,11 +612,11 @@ struct Layout {
 // have not started (ClcLink above).  Grouped launches (whole tiles).
 template <int CTA_GROUP, int BN, int STAGES, int OUT, bool ONE_CHAIN, bool FUSED, int KIND = 0,
           bool GROUPED = false, bool KX2 = false, bool STAGED = false, bool SWAP = false,
-          bool CLC = false>
+          bool CLC = false, bool ADAPT = false>
 __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kThreads), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmC,
-                const GemmParams p) {
+                const GemmParams p, const __grid_constant__ AdaptParams<ADAPT> ad) {
   using L = Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>;
   static_assert(BN == 128 || BN == 256 || BN == 320, "BN must be 128, 256 or 320");
   // 320 columns: two MMAs per K step (N = 256 and N = 64) into one 320-column
@@ -633,6 +633,9 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
                           !GROUPED && !KX2 && !STAGED),
                 "the swapped tiling is a plain CTA-pair kernel with the general epilogue");
   static_assert(!CLC || (GROUPED && !SWAP), "cluster launch control serves grouped launches");
+  static_assert(!ADAPT || (CTA_GROUP == 2 && BN == 256 && !ONE_CHAIN && !FUSED && KIND == 0 &&
+                           !GROUPED && !KX2 && !STAGED && !SWAP),
+                "adapters: a plain CTA-pair kernel of 256 columns with the general epilogue");
   // Accumulator slots in Tensor Memory: two, so that a unit's epilogue overlaps the next
   // chain's MMAs; four for blockwise scales with 128-column tiles, whose chains are one K
   // block each (the MMA then runs up to three K blocks ahead of the epilogue that scales
@@ -851,6 +854,34 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
             phase ^= 1u;
           }
         }
+        if constexpr (ADAPT) {
+          // the tile's adapters: u's two parts, each with the adapter's rows of Up
+          const AdapterTile* at = ad.tiles + w.m_blk;
+          const int32_t slots = w.kb1 == p.k_blocks ? __ldg(&at->slots) : 0;
+          const int32_t parts = ad.rank <= kBlockK ? 2 : 4;  // two for every 64 values of u
+          const CUtensorMap* mapUp = half ? &ad.tmUpHalf : &ad.tmUp;
+          for (int32_t e = 0; ok && e < slots; ++e) {
+            const int32_t up_row = __ldg(&at->slot[e].adapter) * p.N + b_row;
+            for (int32_t x = 0; x < parts; ++x) {
+              if (!warp_wait_inl(empty_bar(stage), phase ^ 1u, ctl, kSiteEmpty)) {
+                ok = false;
+                break;
+              }
+              const uint32_t leader_full = mapa_shared(full_bar(stage), group_base);
+              if (leader) mbar_arrive_expect_tx_elect(full_bar(stage), tx);
+              tma_load_2d_pair_elect(sB + stage * L::kBBytes, mapUp, (x >> 1) * kBlockK, up_row,
+                                     leader_full);
+              tma_load_2d_pair_elect(sA + stage * L::kABytes, &ad.tmU, x * kBlockK, a_row,
+                                     leader_full);
+              armed |= 1u << stage;
+              armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+          }
+        }
         if constexpr (CLC) {
           // Ask for the unit after this one only now that this one's loads are all issued:
           // a unit is claimed as late as the ring still hides the answer's latency (its
@@ -969,6 +1000,43 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
             if constexpr (CTA_GROUP == 1) umma_commit_elect<1>(acc_full_bar(slot));
             else umma_commit_pair_elect(acc_full_bar(slot), pair_mask);
             ++iter;
+          }
+          if constexpr (ADAPT) {
+            const AdapterTile* at = ad.tiles + w.m_blk;
+            const int32_t slots = ok && w.kb1 == p.k_blocks ? __ldg(&at->slots) : 0;
+            if (slots > 0) {
+              const uint32_t slot = iter & (kSlots - 1u), acc_phase = (iter >> kSlotShift) & 1u;
+              if (!warp_wait_inl(acc_empty_bar(slot), acc_phase ^ 1u, ctl, kSiteAccEmpty)) break;
+              tc_fence_after();
+              const uint32_t d_tmem = tmem_base + slot * BN;
+              const int32_t parts = ad.rank <= kBlockK ? 2 : 4;
+              for (int32_t e = 0; ok && e < slots; ++e) {
+                const uint4 off_lo = __ldg(reinterpret_cast<const uint4*>(at->slot[e].disable));
+                const uint4 off_hi = __ldg(reinterpret_cast<const uint4*>(at->slot[e].disable) + 1);
+                for (int32_t x = 0; x < parts; ++x) {
+                  if (!warp_wait_inl(full_bar(stage), phase, ctl, kSiteFull)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+                  const uint64_t da = desc_a0 + ((stage * L::kABytes) >> 4);
+                  const uint64_t db = desc_b0 + ((stage * L::kBBytes) >> 4);
+                  // 16 values of u at a time, as many as the rank has
+                  const int32_t steps = (min(ad.rank - (x >> 1) * kBlockK, kBlockK) + 15) / 16;
+                  for (int32_t k = 0; k < steps; ++k)
+                    umma_pair_masked_elect(d_tmem, da + 2u * (uint32_t)k, db + 2u * (uint32_t)k, idesc,
+                                           (x | k) != 0 ? 1u : 0u, off_lo, off_hi);
+                  umma_commit_pair_elect(empty_bar(stage), stage_mask);
+                  if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                  }
+                }
+              }
+              if (!ok) break;
+              umma_commit_pair_elect(acc_full_bar(slot), pair_mask);
+              ++iter;
+            }
           }
         }
       }
@@ -1158,7 +1226,16 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
       bool final_unit = false;
       if constexpr (STAGED) final_unit = w.nsplit > 1 && !walker_has_next(walk, first_unit, p);
       float acc[kHalf];
-      const int32_t nchains = chains_of(w, p.chain_kb);
+      const int32_t base_chains = chains_of(w, p.chain_kb);
+      int32_t nchains = base_chains;
+      float row_factor = 0.0f;  // (ADAPT) of this thread's row in the adapters' chain
+      if constexpr (ADAPT) {
+        if (w.kb1 == p.k_blocks && __ldg(&ad.tiles[w.m_blk].slots) > 0) {
+          ++nchains;
+          const int32_t m = w.m_blk * kRowsTile + (int32_t)rank * rows_cta + (int32_t)row;
+          if (m < p.M) row_factor = __ldg(ad.row_scale + m);
+        }
+      }
       if constexpr (KIND == 2) {
       // One accumulation chain: wait for it, read it out of Tensor Memory into the fp32
       // registers scaled by sc, hand the slot back.  False when the wait gave up.
@@ -1294,6 +1371,13 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
               if (ch == 0) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[32 * pc + j] = __uint_as_float(r[j]);
+              } else if (ADAPT && ch >= base_chains) {
+                // rows without an adapter: lanes no MMA wrote
+                if (row_factor != 0.0f) {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    acc[32 * pc + j] = fmaf(row_factor, __uint_as_float(r[j]), acc[32 * pc + j]);
+                }
               } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[32 * pc + j] += __uint_as_float(r[j]);

@@ -47,6 +47,12 @@ int max_resident_kx_clusters(int cg, int bn, int stages, int out) {
 
 cudaError_t launch_gemm(const LaunchSpec& s) {
   if (s.clc && !s.grouped) return cudaErrorInvalidValue;
+  if (s.adapt) {
+    if (s.kind != 0 || s.fused || s.grouped || s.kx2 || s.staged || s.swap || s.one_chain ||
+        s.cta_group != 2)
+      return cudaErrorInvalidValue;
+    return launch_cg2_adapt(s);
+  }
   if (s.swap) {
     if (s.kind != 0 || s.fused || s.grouped || s.kx2 || s.staged || s.one_chain || s.cta_group != 2)
       return cudaErrorInvalidValue;

@@ -27,6 +27,8 @@ struct LaunchSpec {
                    // (box bn / 2 rows), C written transposed by direct stores
   bool clc;        // grouped launches: units handed out by cluster launch control (a CTA or
                    // pair per unit in the grid) instead of round-robin over resident ones
+  bool adapt;      // low-rank adapters appended to every tile: ad (CTA pairs, 256 columns)
+  AdaptParams<true> ad;
   CUtensorMap tmA; // A: box {128 bytes of K, 128 (or M < 128) rows}
   CUtensorMap tmB; // B: box {128 bytes of K, bn / cta_group}
   CUtensorMap tmB2; // B: box {128 bytes of K, bn / cta_group / 2} (half-tile units; else tmB);
@@ -97,6 +99,7 @@ cudaError_t launch_cg1_staged(const LaunchSpec& s);  // general epilogue, staged
 cudaError_t launch_cg2_staged(const LaunchSpec& s);
 cudaError_t launch_cg2_swap(const LaunchSpec& s);  // the swapped tiling (kernels_cg2_swap.cu)
 cudaError_t launch_cg2_kxg(const LaunchSpec& s);
+cudaError_t launch_cg2_adapt(const LaunchSpec& s);  // adapters (kernels_cg2_adapt.cu)
 int resident_cg1_kx(int bn, int stages, int out);
 int resident_cg2_kx(int bn, int stages, int out);
 // Clusters of 2 * cta_group CTAs of the cluster-K-split kernel that fit at once (0 if the

@@ -7,9 +7,10 @@ namespace gb300 {
 
 template <int CG, int BN, int STAGES, int OUT, bool ONE, bool FUSED, int KIND = 0,
           bool GROUPED = false, bool KX2 = false, bool STAGED = false, bool SWAP = false,
-          bool CLC = false>
+          bool CLC = false, bool ADAPT = false>
 cudaError_t launch_one(const LaunchSpec& s) {
-  auto kernel = gemm_kernel<CG, BN, STAGES, OUT, ONE, FUSED, KIND, GROUPED, KX2, STAGED, SWAP, CLC>;
+  auto kernel =
+      gemm_kernel<CG, BN, STAGES, OUT, ONE, FUSED, KIND, GROUPED, KX2, STAGED, SWAP, CLC, ADAPT>;
   constexpr unsigned kCluster = CG * (KX2 ? 2 : 1);
   using L = Layout<CG, BN, STAGES, KX2, SWAP>;
   cudaError_t e =
@@ -41,7 +42,10 @@ cudaError_t launch_one(const LaunchSpec& s) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, s.tmA, s.tmB, s.tmB2, s.tmC, s.p);
+  if constexpr (ADAPT)
+    return cudaLaunchKernelEx(&cfg, kernel, s.tmA, s.tmB, s.tmB2, s.tmC, s.p, s.ad);
+  else
+    return cudaLaunchKernelEx(&cfg, kernel, s.tmA, s.tmB, s.tmB2, s.tmC, s.p, AdaptParams<false>{});
 }
 
 template <int CG, int BN, int STAGES, int OUT, bool KX2 = false>
@@ -72,12 +76,13 @@ int resident_one() {
 }
 
 template <int CG, int BN, int STAGES, bool ONE, bool FUSED, int KIND = 0, bool GROUPED = false,
-          bool KX2 = false, bool STAGED = false, bool SWAP = false, bool CLC = false>
+          bool KX2 = false, bool STAGED = false, bool SWAP = false, bool CLC = false,
+          bool ADAPT = false>
 cudaError_t by_out(const LaunchSpec& s) {
   switch (s.out) {
-    case kOutF16: return launch_one<CG, BN, STAGES, kOutF16, ONE, FUSED, KIND, GROUPED, KX2, STAGED, SWAP, CLC>(s);
-    case kOutBF16: return launch_one<CG, BN, STAGES, kOutBF16, ONE, FUSED, KIND, GROUPED, KX2, STAGED, SWAP, CLC>(s);
-    case kOutF32: return launch_one<CG, BN, STAGES, kOutF32, ONE, FUSED, KIND, GROUPED, KX2, STAGED, SWAP, CLC>(s);
+    case kOutF16: return launch_one<CG, BN, STAGES, kOutF16, ONE, FUSED, KIND, GROUPED, KX2, STAGED, SWAP, CLC, ADAPT>(s);
+    case kOutBF16: return launch_one<CG, BN, STAGES, kOutBF16, ONE, FUSED, KIND, GROUPED, KX2, STAGED, SWAP, CLC, ADAPT>(s);
+    case kOutF32: return launch_one<CG, BN, STAGES, kOutF32, ONE, FUSED, KIND, GROUPED, KX2, STAGED, SWAP, CLC, ADAPT>(s);
     default: return cudaErrorInvalidValue;
   }
 }

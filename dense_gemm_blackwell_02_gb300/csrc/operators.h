@@ -69,7 +69,7 @@ cudaError_t launch_logits(LogitsParams p, int elem_in, int elem_out, int sms, cu
 // -------------------------------------------------------------------------- adapters --
 constexpr int kMaxRank = 128;
 constexpr int kAdapterRows = 128;   // rows of X per tile
-constexpr int kAdapterCols = 128;   // columns: of Down . X per group of adapters, of Y per tile
+constexpr int kAdapterCols = 128;   // columns of Down . X per group of adapters
 
 // A batch of few rows (adapters_few_kernel.cu), queued right after the shared product.
 constexpr int kFewRows = 512;
@@ -101,34 +101,26 @@ int few_slices(int32_t M, int32_t K, int32_t rank, int32_t count, int sms);
 cudaError_t launch_adapter_few(const AdapterFewParams& p, int elem_in, int elem_out, int sms,
                                cudaStream_t stream);
 
+// Many rows (adapters_kernel.cu): u of every row and the tiles' adapters, for the GEMM.
 struct AdapterParams {
   const float* scale;   // count, or nullptr
   const int32_t* row_adapter;
   int32_t M, N, K, rank, count;
   int32_t tiles;        // ceil(M / kAdapterRows)
   int32_t k_blocks;     // ceil(K / 64)
-  int32_t x_rows;       // rows of X's box (M, at most 128)
-  int32_t down_ctas;    // CTAs per row tile of the Down product
+  int32_t ctas;         // CTAs per row tile, a cluster: 1, 2, 4 or 8
   int32_t max_splits;   // K slices at most
-  int32_t up_ctas;      // CTAs per row tile of the Up product
-  int32_t vec_store;    // 16-byte accesses of base's and Y's rows are aligned
   uint32_t idesc;       // instruction descriptor without N, 128 rows
-  float* U;             // M x rank: s * Down . x of every row with an adapter
-  float* partial;       // tiles x max_splits x 128 x rank: K slices of u
-  uint32_t* counters;   // tiles x 128: slices that have arrived, zero between calls
-  const float* base;    // M x N: W . x, or nullptr
-  void* Y;              // M x N
+  void* U;              // M x 128 (rank up to 64) or 256 values of the input type
+  float* row_scale;     // M
+  AdapterTile* pairs;   // ceil(tiles / 2)
   uint32_t* status;
   uint64_t wait_limit_ns;
   int32_t test_stall;
 };
 
-// tmX: X, box {64, x_rows}; tmDown: (count * rank) x K, box {64, rank}.
+// tmX: X, box {64, 128}; tmDown: (count * rank) x K, box {64, rank}.
 cudaError_t launch_adapter_down(const CUtensorMap& tmX, const CUtensorMap& tmDown,
-                                const AdapterParams& p, cudaStream_t stream);
-// tmUp: (count * N) x rank, box {64, kAdapterCols}.  base == nullptr: Y is the adapters'
-// term alone, zero for rows without one.
-cudaError_t launch_adapter_up(const CUtensorMap& tmUp, const AdapterParams& p, int elem_in,
-                              int elem_out, cudaStream_t stream);
+                                const AdapterParams& p, int elem_in, cudaStream_t stream);
 
 }  // namespace gb300

@@ -75,7 +75,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   if (M == 0 || N == 0) return GEMM_OK;
   if (!row_adapter || !Y || (K > 0 && (!X || !W))) return GEMM_ERR_INVALID_ARG;
   if (ad->count > 0 && K > 0 && (!ad->down || !ad->up)) return GEMM_ERR_INVALID_ARG;
-  if (M > INT32_MAX - kAdapterRows || N > INT32_MAX - kAdapterCols || K > INT32_MAX)
+  if (M > INT32_MAX - 2 * kAdapterRows || N > INT32_MAX || K > INT32_MAX)
     return GEMM_ERR_UNSUPPORTED;
   if (!aligned(row_adapter, 4) || !aligned(Y, (uint64_t)elem_size(dtype_out))) return GEMM_ERR_UNSUPPORTED;
   if (K == 0 || ad->count == 0)  // nothing to add: the product itself
@@ -83,7 +83,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   if (K % 8 || !aligned(X, 16) || !aligned(W, 16) || !aligned(ad->down, 16) ||
       !aligned(ad->up, 16) || !aligned(ad->scale, 4))
     return GEMM_ERR_UNSUPPORTED;
-  if ((int64_t)ad->count * ad->rank > INT32_MAX || (int64_t)ad->count * N > INT32_MAX)
+  if ((int64_t)ad->count * ad->rank > INT32_MAX || (int64_t)ad->count * N > INT32_MAX - 256)
     return GEMM_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
@@ -122,6 +122,8 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     return launched(h, launch_adapter_few(f, dtype_in, dtype_out, h->sms, stream));
   }
 
+  // Many rows: u of every row and the tiles' adapters first, then the product with the
+  // adapters' term appended to its tiles.
   AdapterParams p;
   std::memset(&p, 0, sizeof(p));
   p.scale = ad->scale;
@@ -133,49 +135,41 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   p.count = ad->count;
   p.tiles = (int32_t)ceil_div(M, kAdapterRows);
   p.k_blocks = (int32_t)ceil_div(K, kBlockK);
-  p.x_rows = (int32_t)std::min<int64_t>(M, kAdapterRows);
-  // Both kernels hold two CTAs per SM.  The CTAs of a row tile share its work, of which
-  // there is at most a K slice of four blocks for every group of adapters, and a column
-  // tile.
-  const int64_t ctas = std::max<int64_t>(1, (int64_t)2 * h->sms / p.tiles);
-  const int64_t per_group = kAdapterCols / p.rank;
-  const int64_t groups = ceil_div(std::min<int64_t>(p.x_rows, ad->count), per_group);
-  p.max_splits = (int32_t)std::min<int64_t>(std::max<int64_t>(1, p.k_blocks / 4), ctas);
-  p.down_ctas = (int32_t)std::min<int64_t>(ctas, groups * p.max_splits);
-  p.up_ctas = (int32_t)std::min<int64_t>(ctas, ceil_div(N, kAdapterCols));
-  p.vec_store = aligned(Y, 16) && (N * elem_size(dtype_out)) % 16 == 0;
+  // As many CTAs per row tile as two on every SM allow (a cluster), each at least four K
+  // blocks of one group of adapters.
+  const int64_t groups = ceil_div(std::min<int64_t>(kAdapterRows, ad->count), kAdapterCols / p.rank);
+  p.max_splits = (int32_t)std::max<int64_t>(1, p.k_blocks / 4);
+  p.ctas = 1;
+  while (p.ctas < 8 && (int64_t)2 * p.ctas * p.tiles <= 2 * h->sms && p.ctas < groups * p.max_splits)
+    p.ctas *= 2;
   p.idesc = idesc_f16_kmajor(kAdapterRows, 0, dtype_in == GEMM_BF16);
-  p.Y = Y;
   p.status = h->d_status;
   p.wait_limit_ns = h->wait_limit_ns;
   p.test_stall = h->test_stall;
-
-  // Scratch: u of every row, its K slices, and (unless Y holds it) the shared product.
-  const size_t u_bytes = round_up((size_t)M * p.rank * sizeof(float));
-  const size_t part_bytes =
-      round_up((size_t)p.tiles * p.max_splits * kAdapterRows * p.rank * sizeof(float));
-  const size_t base_bytes = base_in_y ? 0 : (size_t)M * N * sizeof(float);
-  gemm_status_t st = ensure_scratch(h, u_bytes + part_bytes + base_bytes, (size_t)p.tiles * kAdapterRows);
+  const int64_t pairs = ceil_div(p.tiles, 2), u_cols = 2 * kBlockK * ceil_div(p.rank, kBlockK);
+  const size_t u_bytes = round_up((size_t)M * u_cols * 2);
+  const size_t scale_bytes = round_up((size_t)M * sizeof(float));
+  gemm_status_t st = ensure_scratch(h, u_bytes + scale_bytes + (size_t)pairs * sizeof(AdapterTile), 0);
   if (st != GEMM_OK) return st;
   char* scratch = static_cast<char*>(h->d_op);
-  p.U = reinterpret_cast<float*>(scratch);
-  p.partial = reinterpret_cast<float*>(scratch + u_bytes);
-  p.counters = h->d_op_ctr;
-  void* base = base_in_y ? Y : scratch + u_bytes + part_bytes;
+  p.U = scratch;
+  p.row_scale = reinterpret_cast<float*>(scratch + u_bytes);
+  p.pairs = reinterpret_cast<AdapterTile*>(scratch + u_bytes + scale_bytes);
 
-  CUtensorMap tmX, tmDown, tmUp;
-  if (!make_map(h, X, M, K, dtype_in, p.x_rows, &tmX) ||
+  CUtensorMap tmX, tmDown;
+  AdaptParams<true> g;
+  if (!make_map(h, X, M, K, dtype_in, kAdapterRows, &tmX) ||
       !make_map(h, ad->down, (int64_t)ad->count * p.rank, K, dtype_in, p.rank, &tmDown) ||
-      !make_map(h, ad->up, (int64_t)ad->count * N, p.rank, dtype_in, kAdapterCols, &tmUp))
+      !make_map(h, p.U, M, u_cols, dtype_in, kBlockM, &g.tmU) ||
+      !make_map(h, ad->up, (int64_t)ad->count * N, p.rank, dtype_in, 128, &g.tmUp) ||
+      !make_map(h, ad->up, (int64_t)ad->count * N, p.rank, dtype_in, 64, &g.tmUpHalf))
     return GEMM_ERR_CUDA;
-
-  st = launched(h, launch_adapter_down(tmX, tmDown, p, stream));
-  if (st != GEMM_OK) return st;
-  st = gemm_run(h, X, W, base, M, N, K, dtype_in, GEMM_F32, stream_);
-  if (st != GEMM_OK) return st;
-  p.base = static_cast<const float*>(base);
-  p.vec_store = p.vec_store && N % 4 == 0;  // (base's rows too)
-  return launched(h, launch_adapter_up(tmUp, p, dtype_in, dtype_out, stream));
+  g.tiles = p.pairs;
+  g.row_scale = p.row_scale;
+  g.rank = p.rank;
+  // (the product's configuration is settled before anything is queued)
+  return run_adapted(h, X, W, Y, M, N, K, dtype_in, dtype_out, g,
+                     [&] { return launch_adapter_down(tmX, tmDown, p, dtype_in, stream); }, stream_);
 }
 
 gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t tokens, int64_t heads,

@@ -61,6 +61,32 @@ struct GroupDesc {
   int32_t tma_store;      // C_g is written through tmC
 };
 
+// Adapters inside a product (the ADAPT kernels): the adapters that the rows of a 256-row
+// tile name, and for each the rows that do not name it.
+struct AdapterSlot {
+  int32_t adapter;
+  int32_t pad[3];
+  uint32_t disable[8];    // bit r % 32 of word r / 32: row r of the tile does not name it
+};
+struct AdapterTile {
+  int32_t slots;
+  int32_t pad[3];
+  AdapterSlot slot[2 * kBlockM];
+};
+
+// What an ADAPT kernel takes beside GemmParams; nothing in the others.
+template <bool ADAPT>
+struct AdaptParams {};
+template <>
+struct AdaptParams<true> {
+  CUtensorMap tmU;        // u of every row, M x (128 * chunks): box {64, 128}
+  CUtensorMap tmUp;       // (adapters * N) x rank: box {64, BN / 2}
+  CUtensorMap tmUpHalf;   // ... box {64, BN / 4} (half-tile units)
+  const AdapterTile* tiles;
+  const float* row_scale; // M: the factor of each row's term, 0 without an adapter
+  int32_t rank;
+};
+
 struct GemmParams {
   void* C;                 // M x N row-major output
   int32_t M, N, K;

@@ -410,13 +410,19 @@ __device__ __forceinline__ void umma_commit_pair_elect(uint32_t bar, uint16_t ct
                : "memory");
 }
 
-// One MMA of 16 fp16/bf16 values of K (one CTA); `accumulate` 0 overwrites D.
-__device__ __forceinline__ void umma_f16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate) {
+// One pair MMA of 16 fp16/bf16 values of K that leaves the accumulator rows (lanes of Tensor
+// Memory) whose bits are set in `disable` as they are: words 0..3 for the leader's 128 rows,
+// 4..7 for its peer's.  `accumulate` 0 overwrites the others.
+__device__ __forceinline__ void umma_pair_masked_elect(uint32_t d_tmem, uint64_t a_desc,
+                                                       uint64_t b_desc, uint32_t idesc,
+                                                       uint32_t accumulate, const uint4& lo,
+                                                       const uint4& hi) {
   asm volatile(GB300_ELECT
                ".reg .pred p_;\n\tsetp.ne.b32 p_, %4, 0;\n\t"
-               "@e_ tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p_;\n\t}" ::"r"(d_tmem),
-               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               "@e_ tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, "
+               "{%5, %6, %7, %8, %9, %10, %11, %12}, p_;\n\t}" ::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lo.x), "r"(lo.y),
+               "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
                : "memory");
 }
 
