@@ -23,26 +23,63 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// N elements moved at once: N * sizeof(T) is 16, 32, or the size of one element.
+// N elements moved at once: N * sizeof(T) is 16, 32, or the size of one element.  Kept as
+// loaded until unpack, pairs of 16-bit elements in a register.
 template <typename T, int N>
 struct alignas(N * sizeof(T) >= 16 ? 16 : sizeof(T)) Pack {
   T v[N];
 };
 
+__device__ __forceinline__ float2 pair_f32(__half2 v) { return __half22float2(v); }
+__device__ __forceinline__ float2 pair_f32(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+__device__ __forceinline__ void pair_rn(__half2& d, float a, float b) { d = __floats2half2_rn(a, b); }
+__device__ __forceinline__ void pair_rn(__nv_bfloat162& d, float a, float b) {
+  d = __floats2bfloat162_rn(a, b);
+}
+template <typename T> struct PairOf { using type = __half2; };
+template <> struct PairOf<__nv_bfloat16> { using type = __nv_bfloat162; };
+
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Pack<T, N>& x, float (&f)[N]) {
+  if constexpr (sizeof(T) == 4 || N % 2 != 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_f32(x.v[i]);
+  } else {
+    using P = typename PairOf<T>::type;
+    const P* w = reinterpret_cast<const P*>(&x);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 p = pair_f32(w[i]);
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> pack(const float (&f)[N]) {
+  Pack<T, N> x;
+  if constexpr (sizeof(T) == 4 || N % 2 != 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x.v[i] = from_f32<T>(f[i]);
+  } else {
+    using P = typename PairOf<T>::type;
+    P* w = reinterpret_cast<P*>(&x);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) pair_rn(w[i], f[2 * i], f[2 * i + 1]);
+  }
+  return x;
+}
+
 // A plain (coherent) load: the operators may run in place.
 template <typename T, int N>
 __device__ __forceinline__ void load_f32(const T* p, float (&f)[N]) {
-  const Pack<T, N> x = *reinterpret_cast<const Pack<T, N>*>(p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = to_f32(x.v[i]);
+  unpack(*reinterpret_cast<const Pack<T, N>*>(p), f);
 }
 
 template <typename T, int N>
 __device__ __forceinline__ void store_f32(T* p, const float (&f)[N]) {
-  Pack<T, N> x;
-#pragma unroll
-  for (int i = 0; i < N; ++i) x.v[i] = from_f32<T>(f[i]);
-  *reinterpret_cast<Pack<T, N>*>(p) = x;
+  *reinterpret_cast<Pack<T, N>*>(p) = pack<T, N>(f);
 }
 
 // An index in device memory was out of its range: recorded once, not followed.

@@ -6,9 +6,19 @@
 //
 // A handful of operations per element: bound by HBM, one read and one write of the logits.
 // A CTA owns one slice of one row's vocabulary.  It counts the row's whole history into a
-// table in shared memory, one word per token of its slice (the history is short next to
-// the vocabulary and comes from L2 after the row's first slice), then streams its logits
-// past the table once.  Integer counts: the result does not depend on the atomics' order.
+// table in shared memory, 16 bits per token of its slice (the history is short next to the
+// vocabulary and comes from L2 after the row's first slice), then streams its logits past
+// the table once.  A row that generated more tokens than 14 bits count goes in two halves
+// with 32 bits per token.  Integer counts: the result does not depend on the order of the
+// atomics.
+//
+// 256 x 128256 binary32: 42 us without lists (262 MB at 6.2 TB/s), 60 us with histories of up
+// to 8192 tokens, biases and masks.  Then issue slots bound it (61% busy): some lane of nearly
+// every warp meets a token of the history.  Other forms measured: eight CTAs per SM of half the
+// size, the same; copying first and then rewriting only the logits that the lists name, 70 us
+// (each of the row's slices goes through the history twice); the same from a list of the
+// distinct tokens, 65; the row's CTAs as a cluster that counts in distributed shared memory,
+// 92 (remote atomics).
 #include <algorithm>
 
 #include "elements.cuh"
@@ -20,31 +30,47 @@ namespace gb300 {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kOcc = 3;            // CTAs per SM
 constexpr int kVec = 8;            // logits per thread and step
 constexpr int kTokens = 8;         // history tokens per thread in flight
-constexpr int kMaxSlice = 16384;   // words of table: 64 KiB, three CTAs per SM
+constexpr int kMaxSlice = 24576;   // tokens per CTA: 48 KiB of table
 constexpr int kMinSlice = 2048;
 
-// The table's word of a token: how often it was generated, and two flags.
-constexpr uint32_t kInPrompt = 1u << 31;
-constexpr uint32_t kHasBias = 1u << 30;
-constexpr uint32_t kCount = kHasBias - 1u;
+// A token's entry in the table: how often it was generated, and two flags; 16 bits or 32.
+template <bool WIDE>
+struct Entry {
+  static constexpr uint32_t kInPrompt = WIDE ? 1u << 31 : 1u << 15;
+  static constexpr uint32_t kHasBias = WIDE ? 1u << 30 : 1u << 14;
+  static constexpr uint32_t kCount = kHasBias - 1u;
+  static __device__ __forceinline__ void add(uint32_t* table, int32_t at) {
+    if constexpr (WIDE) atomicAdd(table + at, 1u);
+    else atomicAdd(table + (at >> 1), 1u << (16 * (at & 1)));
+  }
+  static __device__ __forceinline__ void flag(uint32_t* table, int32_t at, uint32_t f) {
+    if constexpr (WIDE) atomicOr(table + at, f);
+    else atomicOr(table + (at >> 1), f << (16 * (at & 1)));
+  }
+};
 
 struct RowRules {
   float rep, freq, pres;
+  int64_t t0, t1, said;  // the row's history, and where its generated part begins
   int64_t bias0, bias1;
+  const uint32_t* mask;
 };
 
-// One logit through the penalties and biases its word calls for.
-__device__ __forceinline__ float adjust(float z, uint32_t word, int32_t v, const RowRules& r,
+// A token's logit through the penalties and biases its entry calls for.
+template <bool WIDE>
+__device__ __forceinline__ float adjust(float z, uint32_t entry, int32_t v, const RowRules& r,
                                         const LogitsParams& p) {
-  if (word & ~kHasBias) {
+  using E = Entry<WIDE>;
+  if (entry & ~E::kHasBias) {
     z = z > 0.0f ? __fdiv_rn(z, r.rep) : z * r.rep;
-    const uint32_t c = word & kCount;
+    const uint32_t c = entry & E::kCount;
     if (c) z = z - r.freq * (float)c - r.pres;
   }
-  if (word & kHasBias) {
-    int64_t lo = r.bias0, hi = r.bias1;  // the first entry not below v
+  if (entry & E::kHasBias) {
+    int64_t lo = r.bias0, hi = r.bias1;  // the first of the token's
     while (lo < hi) {
       const int64_t mid = lo + (hi - lo) / 2;
       if (p.bias_tokens[mid] < v) lo = mid + 1;
@@ -57,9 +83,101 @@ __device__ __forceinline__ float adjust(float z, uint32_t word, int32_t v, const
   return z;
 }
 
+// Positions w0..w1-1 of a row (w0 a multiple of kVec; position w is token w - shift): the
+// table, then the logits.
+template <typename TI, typename TO, bool TABLE, bool WIDE>
+__device__ __forceinline__ void do_slice(const LogitsParams& p, const RowRules& r, const TI* in,
+                                         TO* out, int32_t shift, bool vec, int32_t w0, int32_t w1,
+                                         uint32_t* table) {
+  // The first logits are on their way while the table is built, and every step's while the
+  // one before is worked on; kept as loaded.
+  auto whole = [&](int32_t w) { return w >= shift && w - shift + kVec <= p.vocab; };
+  Pack<TI, kVec> next;
+  const int32_t first = w0 + (int32_t)threadIdx.x * kVec;
+  if (vec && first < w1 && whole(first)) next = *reinterpret_cast<const Pack<TI, kVec>*>(in + first - shift);
+
+  if constexpr (TABLE) {
+    uint4* t4 = reinterpret_cast<uint4*>(table);
+    const int32_t quads = (w1 - w0 + (WIDE ? 3 : 7)) / (WIDE ? 4 : 8);
+    for (int32_t i = (int32_t)threadIdx.x; i < quads; i += kThreads) t4[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const uint32_t lo = (uint32_t)max(w0 - shift, 0), hi = (uint32_t)(w1 - shift);  // its tokens
+    for (int64_t i0 = r.t0 + threadIdx.x; i0 < r.t1; i0 += kThreads * kTokens) {
+      uint32_t v[kTokens];
+#pragma unroll
+      for (int j = 0; j < kTokens; ++j)
+        v[j] = i0 + j * kThreads < r.t1 ? (uint32_t)__ldg(p.tokens + i0 + j * kThreads) : 0xFFFFFFFFu;
+#pragma unroll
+      for (int j = 0; j < kTokens; ++j) {
+        if (v[j] < lo || v[j] >= hi) continue;  // padding, or another slice's
+        const int32_t at = (int32_t)v[j] + shift - w0;
+        if (i0 + j * kThreads >= r.said) Entry<WIDE>::add(table, at);
+        else Entry<WIDE>::flag(table, at, Entry<WIDE>::kInPrompt);
+      }
+    }
+    for (int64_t i = r.bias0 + threadIdx.x; i < r.bias1; i += kThreads) {
+      const uint32_t v = (uint32_t)__ldg(p.bias_tokens + i);
+      if (v >= lo && v < hi) Entry<WIDE>::flag(table, (int32_t)v + shift - w0, Entry<WIDE>::kHasBias);
+    }
+    __syncthreads();
+  }
+
+  for (int32_t w = first; w < w1; w += kThreads * kVec) {
+    const int32_t v = w - shift;  // the first of kVec tokens; below 0 or past the end: none
+    float z[kVec];
+    if (vec && whole(w)) {
+      unpack(next, z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        z[j] = v + j >= 0 && v + j < p.vocab ? to_f32(in[v + j]) : 0.0f;
+    }
+    const int32_t ahead = w + kThreads * kVec;
+    if (vec && ahead < w1 && whole(ahead))
+      next = *reinterpret_cast<const Pack<TI, kVec>*>(in + ahead - shift);
+    if constexpr (TABLE) {
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const uint32_t entry = table[w - w0 + j];
+          if (entry) z[j] = adjust<WIDE>(z[j], entry, v + j, r, p);
+        }
+      } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(table + (w - w0) / 2);
+        if (a.x | a.y | a.z | a.w) {
+          const uint32_t two[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) {
+            const uint32_t entry = (two[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+            if (entry) z[j] = adjust<WIDE>(z[j], entry, v + j, r, p);
+          }
+        }
+      }
+    }
+    if (r.mask) {
+      // bit j: token v + j may follow
+      const int32_t last = (p.vocab - 1) >> 5;
+      const int32_t lo = v >> 5;  // (floor: -1 when v < 0)
+      const uint32_t word0 = lo >= 0 ? __ldg(r.mask + lo) : 0u;
+      const uint32_t word1 = lo < last && (v & 31) > 32 - kVec ? __ldg(r.mask + lo + 1) : 0u;
+      const uint32_t bits = __funnelshift_r(word0, word1, (uint32_t)(v & 31));
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (!((bits >> j) & 1u)) z[j] = __int_as_float(0xff800000);
+    }
+    if (vec && whole(w)) {
+      store_f32<TO, kVec>(out + v, z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (v + j >= 0 && v + j < p.vocab && w + j < w1) out[v + j] = from_f32<TO>(z[j]);
+    }
+  }
+}
+
 // TABLE: there are histories or biases to look up.
 template <typename TI, typename TO, bool TABLE>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ LogitsParams p) {
+__global__ void __launch_bounds__(kThreads, kOcc) logits_kernel(const __grid_constant__ LogitsParams p) {
   extern __shared__ __align__(16) uint32_t table[];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -68,113 +186,52 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   const int32_t part = (int32_t)(blockIdx.x - (uint32_t)row * (uint32_t)p.slices);
   const TI* in = static_cast<const TI*>(p.in) + (int64_t)row * p.in_stride;
   TO* out = static_cast<TO*>(p.out) + (int64_t)row * p.out_stride;
-  // Rows of any alignment: positions are counted from the 16-byte boundary of the vectors
-  // below the row's start, w = v + shift, so that vectors of kVec positions are aligned
-  // (in input and output alike, else single elements are moved).
+  // Rows of any alignment: positions are counted from the boundary of kVec elements below
+  // the row's start, w = v + shift, so that vectors of positions are aligned (in input and
+  // output alike, else single elements are moved).
   const int32_t shift = (int32_t)((reinterpret_cast<uintptr_t>(in) / sizeof(TI)) % kVec);
   const bool vec = (int32_t)((reinterpret_cast<uintptr_t>(out) / sizeof(TO)) % kVec) == shift;
   const int32_t w0 = part * p.slice, w1 = min(w0 + p.slice, p.vocab + shift);
   if (w0 >= w1) return;  // (the last slice of a row with a small shift)
 
-  RowRules r{1.0f, 0.0f, 0.0f, 0, 0};
-  if constexpr (TABLE) {
-    uint4* t4 = reinterpret_cast<uint4*>(table);
-    for (int32_t i = (int32_t)threadIdx.x; i < p.slice / 4; i += kThreads) t4[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (p.tokens) {
-      if (p.repetition) r.rep = p.repetition[row];
-      if (p.frequency) r.freq = p.frequency[row];
-      if (p.presence) r.pres = p.presence[row];
-      const int64_t t0 = p.token_start[row], t1 = p.token_start[row + 1];
-      const int64_t said = t0 + (p.prompt_len ? p.prompt_len[row] : 0);
-      for (int64_t i0 = t0; i0 < t1; i0 += kThreads * kTokens) {
-        int32_t v[kTokens];
-#pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-          const int64_t i = i0 + j * kThreads + threadIdx.x;
-          v[j] = i < t1 ? __ldg(p.tokens + i) : -1;
-        }
-#pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-          const int32_t w = v[j] + shift - w0;
-          if (v[j] < 0 || v[j] >= p.vocab || w < 0 || w >= p.slice) continue;  // padding, or another slice's
-          if (i0 + j * kThreads + threadIdx.x >= said) atomicAdd(table + w, 1u);
-          else atomicOr(table + w, kInPrompt);
-        }
-      }
-    }
-    if (p.bias_tokens) {
-      r.bias0 = p.bias_start[row];
-      r.bias1 = p.bias_start[row + 1];
-      for (int64_t i = r.bias0 + threadIdx.x; i < r.bias1; i += kThreads) {
-        const int32_t v = p.bias_tokens[i];
-        if (v < 0 || v >= p.vocab) continue;
-        const int32_t w = v + shift - w0;
-        if (w >= 0 && w < p.slice) atomicOr(table + w, kHasBias);
-      }
-    }
-    __syncthreads();
+  RowRules r{1.0f, 0.0f, 0.0f, 0, 0, 0, 0, 0, nullptr};
+  if (p.tokens) {
+    r.t0 = p.token_start[row];
+    r.t1 = p.token_start[row + 1];
+    r.said = r.t0 + (p.prompt_len ? p.prompt_len[row] : 0);
+    if (p.repetition) r.rep = p.repetition[row];
+    if (p.frequency) r.freq = p.frequency[row];
+    if (p.presence) r.pres = p.presence[row];
   }
-
-  const uint32_t* mask = nullptr;
+  if (p.bias_tokens) {
+    r.bias0 = p.bias_start[row];
+    r.bias1 = p.bias_start[row + 1];
+  }
   if (p.mask) {
     const int64_t m = p.mask_row ? p.mask_row[row] : row;
     if (m >= p.mask_count) {
       if (threadIdx.x == 0) record_bad_index(p.status, kSiteMaskRow);
     } else if (m >= 0) {
-      mask = p.mask + m * p.mask_stride;
+      r.mask = p.mask + m * p.mask_stride;
     }
   }
-
-  for (int32_t w = w0 + (int32_t)threadIdx.x * kVec; w < w1; w += kThreads * kVec) {
-    const int32_t v = w - shift;  // the first of kVec tokens; below 0 or past the end: none
-    const bool whole = v >= 0 && v + kVec <= p.vocab;
-    float z[kVec];
-    if (vec && whole) {
-      load_f32<TI, kVec>(in + v, z);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        z[j] = v + j >= 0 && v + j < p.vocab ? to_f32(in[v + j]) : 0.0f;
-    }
-    if constexpr (TABLE) {
-      const uint4 a = *reinterpret_cast<const uint4*>(table + (w - w0));
-      const uint4 b = *reinterpret_cast<const uint4*>(table + (w - w0) + 4);
-      const uint32_t word[kVec] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      if (a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-          if (word[j]) z[j] = adjust(z[j], word[j], v + j, r, p);
-      }
-    }
-    if (mask) {
-      uint32_t bits = 0;  // bit j: token v + j may follow
-      const int32_t last = (p.vocab - 1) >> 5;
-      const int32_t lo = v >> 5;  // (floor: -1 when v < 0)
-      const uint32_t word0 = lo >= 0 ? __ldg(mask + lo) : 0u;
-      const uint32_t word1 = lo < last && (v & 31) > 32 - kVec ? __ldg(mask + lo + 1) : 0u;
-      bits = __funnelshift_r(word0, word1, (uint32_t)(v & 31));
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (!((bits >> j) & 1u)) z[j] = __int_as_float(0xff800000);
-    }
-    if (vec && whole) {
-      store_f32<TO, kVec>(out + v, z);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (v + j >= 0 && v + j < p.vocab) out[v + j] = from_f32<TO>(z[j]);
-    }
+  if (!TABLE || r.t1 - r.said <= (int64_t)Entry<false>::kCount) {
+    do_slice<TI, TO, TABLE, false>(p, r, in, out, shift, vec, w0, w1, table);
+  } else {
+    const int32_t mid = min(w0 + p.slice / 2, w1);
+    do_slice<TI, TO, TABLE, true>(p, r, in, out, shift, vec, w0, mid, table);
+    __syncthreads();
+    if (mid < w1) do_slice<TI, TO, TABLE, true>(p, r, in, out, shift, vec, mid, w1, table);
   }
 }
 
 template <typename TI, typename TO, bool TABLE>
 cudaError_t launch(const LogitsParams& p, cudaStream_t stream) {
-  const size_t smem = TABLE ? (size_t)p.slice * sizeof(uint32_t) : 0;
+  const size_t smem = TABLE ? (size_t)p.slice * 2 : 0;
   auto kernel = logits_kernel<TI, TO, TABLE>;
   if (TABLE) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxSlice * (int)sizeof(uint32_t));
+                                               kMaxSlice * 2);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -208,16 +265,15 @@ cudaError_t by_out(const LogitsParams& p, int elem_out, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_logits(LogitsParams p, int elem_in, int elem_out, int sms, cudaStream_t stream) {
-  // Slices as long as the table allows, so that few CTAs read the same history; shorter
-  // ones where the rows alone do not give every SM two CTAs.
+  // Slices as long as the table allows; shorter ones where the rows alone do not give every
+  // SM two CTAs.
   const int64_t width = (int64_t)p.vocab + kVec - 1;  // with the largest shift
   const int64_t want = std::max<int64_t>(1, ((int64_t)2 * sms + p.rows - 1) / p.rows);
   int64_t slice = (width + want - 1) / want;
   slice = std::min<int64_t>(std::max<int64_t>(slice, kMinSlice), kMaxSlice);
-  const int64_t n = (width + slice - 1) / slice;
-  slice = ((width + n - 1) / n + 31) / 32 * 32;  // even slices
-  p.slice = (int32_t)slice;
-  p.slices = (int32_t)((width + slice - 1) / slice);
+  int64_t n = (width + slice - 1) / slice;
+  p.slice = (int32_t)(((width + n - 1) / n + 63) / 64 * 64);  // even slices, of even halves
+  p.slices = (int32_t)((width + p.slice - 1) / p.slice);
   switch (elem_in) {
     case kElemF16: return by_out<__half>(p, elem_out, stream);
     case kElemBF16: return by_out<__nv_bfloat16>(p, elem_out, stream);

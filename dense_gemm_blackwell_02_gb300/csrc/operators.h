@@ -22,8 +22,9 @@ struct RotaryParams {
   int64_t x_token, x_head, y_token, y_head;  // strides in elements
   int32_t tokens, heads, dim, half;          // half: pairs per head
   int32_t inverse;
-  int32_t head_run;     // consecutive heads of one token that a thread turns
-  int32_t head_runs;    // ceil(heads / head_run)
+  int32_t tile_tokens;  // tokens per CTA
+  int32_t shares;       // CTAs per tile of tokens,
+  int32_t share_heads;  // each this many heads
   int32_t items;        // work items per head: vectors of pairs, then vectors to copy
   const float* cos;
   const float* sin;
@@ -34,7 +35,7 @@ struct RotaryParams {
 };
 
 // vec: 16-byte accesses of x, y and the tables are aligned and no vector straddles the
-// pairs' end.  head_run, head_runs and items are filled in here.
+// pairs' end.  The split into CTAs is filled in here.
 cudaError_t launch_rotary(RotaryParams p, int elem, bool neighbours, bool vec, int sms,
                           cudaStream_t stream);
 int rotary_vector(int elem);  // elements of a 16-byte vector
@@ -46,7 +47,7 @@ struct LogitsParams {
   int64_t in_stride, out_stride;
   int32_t rows;
   int32_t vocab;
-  int32_t slice;    // vocabulary entries per CTA (a multiple of 32)
+  int32_t slice;    // vocabulary entries per CTA (a multiple of 64)
   int32_t slices;   // CTAs per row
   const int32_t* tokens;
   const int64_t* token_start;
@@ -63,7 +64,7 @@ struct LogitsParams {
   uint32_t* status;
 };
 
-// slice and slices are filled in here.
+// The split into CTAs is filled in here.
 cudaError_t launch_logits(LogitsParams p, int elem_in, int elem_out, int sms, cudaStream_t stream);
 
 // -------------------------------------------------------------------------- adapters --

@@ -225,8 +225,7 @@ gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t token
   // end) and the head's end fall on one.
   const bool neigh = r->pairs == GEMM_PAIRS_NEIGHBOURS;
   const int64_t v = rotary_vector(dtype);
-  const bool vec = aligned(x, 16) && aligned(y, 16) && aligned(r->cos, 16) && aligned(r->sin, 16) &&
-                   half % 4 == 0 &&
+  const bool vec = aligned(x, 16) && aligned(y, 16) && half % 4 == 0 &&
                    (x_token_stride | x_head_stride | y_token_stride | y_head_stride) % v == 0 &&
                    (neigh ? 2 * half : half) % v == 0 && (dim - 2 * half) % v == 0;
   return launched(h, launch_rotary(p, dtype, neigh, vec, h->sms, reinterpret_cast<cudaStream_t>(stream_)));

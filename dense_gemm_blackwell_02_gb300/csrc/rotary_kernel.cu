@@ -4,10 +4,11 @@
 // in binary32, rounded once to the element type.
 //
 // Six operations per pair against 4 elements moved: bound by HBM, so the kernel is one
-// pass of 16-byte accesses.  A thread owns one vector of pairs of a head (two vectors of
-// the head when a pair's halves lie apart, one when they are neighbours), reads its
-// cosines and sines once, and turns that vector in `head_run` consecutive heads of the
-// token, whose loads are all issued before the first use.
+// pass of 16-byte accesses.  A CTA takes the heads of a few tokens.  It first gathers the
+// tokens' cosines and sines, pair by pair from the rows that the pairs' axes ask for, into
+// shared memory, while the first elements are already on their way; then every thread owns
+// one vector of pairs of a head (two vectors of the head when a pair's halves lie apart, one
+// when they are neighbours) and walks the heads, several loads in flight.
 #include <algorithm>
 
 #include "elements.cuh"
@@ -19,142 +20,167 @@ namespace gb300 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRun = 4;  // heads whose loads are in flight together
+constexpr int kRun = 3;         // heads whose loads are in flight together, per thread
+constexpr int kMaxTokens = 8;   // tokens per CTA at most
 
-// Whether one axis turns N pairs, whose bytes start at a multiple of N.
-template <int N>
-__device__ __forceinline__ bool one_axis(const uint8_t* axis) {
-  if constexpr (N == 8) {
-    const uint2 w = *reinterpret_cast<const uint2*>(axis);
-    return w.x == w.y && w.x == (w.x & 0xFFu) * 0x01010101u;
-  } else if constexpr (N == 4) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(axis);
-    return w == (w & 0xFFu) * 0x01010101u;
-  } else {
-    return N == 2 ? axis[0] == axis[1] : true;
-  }
-}
-
-// N values of a table's row (16-byte aligned for N >= 4, 8-byte for 2).
+// N neighbouring values of the table (16-byte aligned for N >= 4, 8-byte for 2).
 template <int N>
 __device__ __forceinline__ void load_row(const float* p, float (&f)[N]) {
   if constexpr (N >= 4) {
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p + j));
+      const float4 v = *reinterpret_cast<const float4*>(p + j);
       f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
     }
   } else if constexpr (N == 2) {
-    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+    const float2 v = *reinterpret_cast<const float2*>(p);
     f[0] = v.x, f[1] = v.y;
   } else {
-    f[0] = __ldg(p);
+    f[0] = *p;
   }
 }
 
 // NEIGH: neighbouring pairs.  V: elements per vector (1: no alignment is assumed).
 template <typename T, bool NEIGH, int V>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
   // pairs per item: V with the halves apart (two vectors), V / 2 as neighbours (one; with
   // V = 1 two single elements)
   constexpr int kPairs = NEIGH ? (V > 1 ? V / 2 : 1) : V;
   constexpr int kSpan = NEIGH ? 2 * kPairs : V;  // elements of one access
+  extern __shared__ __align__(16) float table[];  // per token: half cosines, half sines
   grid_dependency_wait();
   grid_launch_dependents();
 
-  const int lanes = min(p.items, kThreads);        // threads per (token, run of heads)
-  const int groups = kThreads / lanes;             // ... of which a CTA holds this many
+  const int32_t tile = (int32_t)(blockIdx.x / (uint32_t)p.shares);
+  const int32_t share = (int32_t)(blockIdx.x - (uint32_t)tile * (uint32_t)p.shares);
+  const int32_t t0 = tile * p.tile_tokens, nt = min(p.tile_tokens, p.tokens - t0);
+  const int32_t h0 = share * p.share_heads, nh = min(p.share_heads, p.heads - h0);
+  const int lanes = min(p.items, kThreads);   // threads per head
+  const int groups = kThreads / lanes;        // heads at a time
   const int g = (int)threadIdx.x / lanes;
-  if (g >= groups) return;
-  const int64_t q = (int64_t)blockIdx.x * groups + g;
-  const int32_t t = (int32_t)(q / p.head_runs);
-  if (t >= p.tokens) return;
-  const int32_t h0 = (int32_t)(q - (int64_t)t * p.head_runs) * p.head_run;
-  const int32_t nh = min(p.head_run, p.heads - h0);
-  const T* x = static_cast<const T*>(p.x) + (int64_t)t * p.x_token + (int64_t)h0 * p.x_head;
-  T* y = static_cast<T*>(p.y) + (int64_t)t * p.y_token + (int64_t)h0 * p.y_head;
-  const int pair_items = (p.half + kPairs - 1) / kPairs;  // (exact unless V is 1)
+  const int pair_items = p.half / kPairs;
+  const T* x = static_cast<const T*>(p.x) + (int64_t)t0 * p.x_token + (int64_t)h0 * p.x_head;
+  T* y = static_cast<T*>(p.y) + (int64_t)t0 * p.y_token + (int64_t)h0 * p.y_head;
+  const int rows = nt * nh;                   // heads of all tokens
+  // A thread's heads are `groups` apart: tokens and heads onward, and back at a token's end.
+  const int step_t = groups / nh, step_h = groups - step_t * nh;
+  struct Cursor {
+    const T* x;
+    T* y;
+    int t, h, r;
+  };
+  auto advance = [&](Cursor& c) {
+    c.r += groups;
+    c.t += step_t;
+    c.h += step_h;
+    c.x += step_t * p.x_token + step_h * p.x_head;
+    c.y += step_t * p.y_token + step_h * p.y_head;
+    if (c.h >= nh) {
+      c.h -= nh;
+      ++c.t;
+      c.x += p.x_token - nh * p.x_head;
+      c.y += p.y_token - nh * p.y_head;
+    }
+  };
+  Pack<T, kSpan> a[kRun], b[kRun];
 
-  for (int item = (int)threadIdx.x - g * lanes; item < p.items; item += lanes) {
-    if (item >= pair_items) {
-      // past the pairs: copied, unless the operator runs in place
-      if (static_cast<const void*>(p.x) == p.y) continue;
-      const int d = 2 * p.half + (item - pair_items) * V;
-      for (int k = 0; k < nh; ++k)
-        *reinterpret_cast<Pack<T, V>*>(y + k * p.y_head + d) =
-            *reinterpret_cast<const Pack<T, V>*>(x + k * p.x_head + d);
-      continue;
-    }
-    const int i0 = item * kPairs;
-    const int d0 = NEIGH ? 2 * i0 : i0, d1 = i0 + p.half;  // (d1: second halves)
-    float a[kMaxRun][kSpan], b[kMaxRun][NEIGH ? 1 : kSpan];
+  // The next kRun heads of an item, as loaded ...
+  auto load = [&](int item, Cursor c) {
 #pragma unroll
-    for (int k = 0; k < kMaxRun; ++k) {
-      if (k >= nh) break;
-      if constexpr (NEIGH && V == 1) {
-        a[k][0] = to_f32(x[k * p.x_head + d0]);
-        a[k][1] = to_f32(x[k * p.x_head + d0 + 1]);
+    for (int k = 0; k < kRun; ++k) {
+      if (c.r >= rows) break;
+      if (item >= pair_items) {  // past the pairs: copied
+        *reinterpret_cast<Pack<T, V>*>(&a[k]) =
+            *reinterpret_cast<const Pack<T, V>*>(c.x + 2 * p.half + (item - pair_items) * V);
+      } else if constexpr (NEIGH && V == 1) {
+        a[k].v[0] = c.x[2 * item];
+        a[k].v[1] = c.x[2 * item + 1];
       } else {
-        load_f32<T, kSpan>(x + k * p.x_head + d0, a[k]);
-        if constexpr (!NEIGH) load_f32<T, kSpan>(x + k * p.x_head + d1, b[k]);
+        a[k] = *reinterpret_cast<const Pack<T, kSpan>*>(c.x + item * kSpan);
+        if constexpr (!NEIGH) b[k] = *reinterpret_cast<const Pack<T, kSpan>*>(c.x + item * kSpan + p.half);
       }
+      advance(c);
     }
-    float c[kPairs], s[kPairs];
-    if (V > 1 && one_axis<kPairs>(p.pair_axis + i0)) {
-      // one position for the whole vector: its cosines and sines stand in a row
-      const int64_t pos = p.positions[(int64_t)p.pair_axis[i0] * p.tokens + t];
-      if (pos >= 0 && pos < p.num_positions) {
-        load_row<kPairs>(p.cos + pos * p.half + i0, c);
-        load_row<kPairs>(p.sin + pos * p.half + i0, s);
-      } else {
-        record_bad_index(p.status, kSitePosition);
+  };
+  // ... and turned; the cursor moves on.
+  auto finish = [&](int item, Cursor& c) {
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) c[j] = 1.0f, s[j] = 0.0f;
+    for (int k = 0; k < kRun; ++k) {
+      if (c.r >= rows) break;
+      if (item >= pair_items) {
+        *reinterpret_cast<Pack<T, V>*>(c.y + 2 * p.half + (item - pair_items) * V) =
+            *reinterpret_cast<const Pack<T, V>*>(&a[k]);
+        advance(c);
+        continue;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPairs; ++j) {
-        const int64_t pos = p.positions[(int64_t)p.pair_axis[i0 + j] * p.tokens + t];
-        c[j] = 1.0f;
-        s[j] = 0.0f;
-        if (pos >= 0 && pos < p.num_positions) {
-          c[j] = __ldg(p.cos + pos * p.half + i0 + j);
-          s[j] = __ldg(p.sin + pos * p.half + i0 + j);
-        } else {
-          record_bad_index(p.status, kSitePosition);
-        }
-      }
-    }
-    if (p.inverse) {
-#pragma unroll
-      for (int j = 0; j < kPairs; ++j) s[j] = -s[j];
-    }
-#pragma unroll
-    for (int k = 0; k < kMaxRun; ++k) {
-      if (k >= nh) break;
+      const float* row = table + c.t * 2 * p.half + item * kPairs;
+      float cs[kPairs], sn[kPairs];
+      load_row<kPairs>(row, cs);
+      load_row<kPairs>(row + p.half, sn);
+      T* at = c.y + item * kSpan;
       if constexpr (NEIGH) {
-        float r[kSpan];
+        float in[kSpan], o[kSpan];
+        if constexpr (V == 1) in[0] = to_f32(a[k].v[0]), in[1] = to_f32(a[k].v[1]);
+        else unpack(a[k], in);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          r[2 * j] = a[k][2 * j] * c[j] - a[k][2 * j + 1] * s[j];
-          r[2 * j + 1] = a[k][2 * j + 1] * c[j] + a[k][2 * j] * s[j];
+          const float u = in[2 * j], v = in[2 * j + 1];
+          o[2 * j] = u * cs[j] - v * sn[j];
+          o[2 * j + 1] = v * cs[j] + u * sn[j];
         }
         if constexpr (V == 1) {
-          y[k * p.y_head + d0] = from_f32<T>(r[0]);
-          y[k * p.y_head + d0 + 1] = from_f32<T>(r[1]);
+          at[0] = from_f32<T>(o[0]);
+          at[1] = from_f32<T>(o[1]);
         } else {
-          store_f32<T, kSpan>(y + k * p.y_head + d0, r);
+          store_f32<T, kSpan>(at, o);
         }
       } else {
-        float ra[kSpan], rb[kSpan];
+        float u[kSpan], v[kSpan], oa[kSpan], ob[kSpan];
+        unpack(a[k], u);
+        unpack(b[k], v);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          ra[j] = a[k][j] * c[j] - b[k][j] * s[j];
-          rb[j] = b[k][j] * c[j] + a[k][j] * s[j];
+          oa[j] = u[j] * cs[j] - v[j] * sn[j];
+          ob[j] = v[j] * cs[j] + u[j] * sn[j];
         }
-        store_f32<T, kSpan>(y + k * p.y_head + d0, ra);
-        store_f32<T, kSpan>(y + k * p.y_head + d1, rb);
+        store_f32<T, kSpan>(at, oa);
+        store_f32<T, kSpan>(at + p.half, ob);
       }
+      advance(c);
+    }
+  };
+  Cursor start;
+  start.r = g;
+  start.t = g / nh;
+  start.h = g - start.t * nh;
+  start.x = x + start.t * p.x_token + start.h * p.x_head;
+  start.y = y + start.t * p.y_token + start.h * p.y_head;
+
+  const bool works = g < groups;
+  int item = (int)threadIdx.x - g * lanes;
+  // (in place there is nothing to do past the pairs)
+  const int items = static_cast<const void*>(p.x) == p.y ? pair_items : p.items;
+  if (works && item < items) load(item, start);
+  for (int i = (int)threadIdx.x; i < nt * p.half; i += kThreads) {
+    const int t = i / p.half, pair = i - t * p.half;
+    const int64_t pos = p.positions[(int64_t)p.pair_axis[pair] * p.tokens + t0 + t];
+    float c = 1.0f, s = 0.0f;
+    if (pos >= 0 && pos < p.num_positions) {
+      c = __ldg(p.cos + pos * p.half + pair);
+      s = __ldg(p.sin + pos * p.half + pair);
+    } else {
+      record_bad_index(p.status, kSitePosition);
+    }
+    table[t * 2 * p.half + pair] = c;
+    table[t * 2 * p.half + p.half + pair] = p.inverse ? -s : s;
+  }
+  __syncthreads();
+  if (!works) return;
+  for (; item < items; item += lanes) {
+    Cursor c = start;
+    while (c.r < rows) {
+      if (c.r != g || item >= lanes) load(item, c);
+      finish(item, c);
     }
   }
 }
@@ -164,20 +190,22 @@ cudaError_t launch(RotaryParams& p, int sms, cudaStream_t stream) {
   const int pairs = NEIGH ? (V > 1 ? V / 2 : 1) : V;
   p.items = p.half / pairs + (p.dim - 2 * p.half) / V;
   const int groups = kThreads / std::min(p.items, kThreads);
-  // As many heads per thread as keep every SM busy with four CTAs; fewer tokens than that
-  // spread their heads over more threads.
-  p.head_run = 1;
-  for (int run = kMaxRun; run > 1; run /= 2)
-    if ((int64_t)p.tokens * ((p.heads + run - 1) / run) >= (int64_t)4 * sms * groups) {
-      p.head_run = run;
-      break;
-    }
-  p.head_runs = (p.heads + p.head_run - 1) / p.head_run;
-  p.head_run = (p.heads + p.head_runs - 1) / p.head_runs;  // even runs
-  const int64_t blocks = ((int64_t)p.tokens * p.head_runs + groups - 1) / groups;
+  // A CTA takes as many tokens as give every thread three runs of heads, as long as every
+  // SM has two CTAs; with fewer tokens than that, shares of one token's heads.  (8192 x 72 x
+  // 128 bf16: one run 70 us, two 55.6, three 53.1, six 58.9.  256 x 72 x 128: 4.6 us, with
+  // smaller CTAs, eight to an SM, 6.3.)
+  const int64_t want = (int64_t)3 * kRun * groups;  // heads per CTA
+  const int64_t spread = ((int64_t)p.tokens * p.heads + 2 * sms - 1) / (2 * sms);
+  const int64_t per_cta = std::max<int64_t>(groups, std::min(want, spread));
+  p.tile_tokens = (int32_t)std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, per_cta / p.heads));
+  p.shares = (int32_t)((p.heads + per_cta - 1) / per_cta);
+  p.share_heads = (p.heads + p.shares - 1) / p.shares;
+  p.shares = (p.heads + p.share_heads - 1) / p.share_heads;
+  const int64_t tiles = ((int64_t)p.tokens + p.tile_tokens - 1) / p.tile_tokens;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+  cfg.gridDim = dim3((unsigned)(tiles * p.shares), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)p.tile_tokens * 2 * p.half * sizeof(float);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
