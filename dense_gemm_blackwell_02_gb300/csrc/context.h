@@ -49,6 +49,7 @@ struct gemm_ctx {
   uint32_t* d_op_ctr = nullptr;
   size_t op_ctr_count = 0;
   gemm_config_t forced = {};
+  int32_t short_chains = 0;  // K blocks per accumulation chain where none is forced (0: the default)
   gemm_config_t last = {};
   uint64_t wait_limit_ns = 2000000000ull;
   int32_t test_stall = 0;

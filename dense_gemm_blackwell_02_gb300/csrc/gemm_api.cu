@@ -123,6 +123,9 @@ int kx_clusters(gemm_ctx* h, int cg, int bn, int stages, int out) {
 
 // The default accumulation chain: K 4096 elements, 64 blocks of fp16/bf16, 32 of FP8.
 int64_t chain_kb_of(int kb_elems) { return kChainKBlocks * kBlockK / kb_elems; }
+int default_chain(const gemm_ctx* h, int kb_elems) {
+  return h->short_chains ? h->short_chains : (int)chain_kb_of(kb_elems);
+}
 
 // kb_elems: K elements per 128-byte K block (64 fp16/bf16, 128 FP8).
 // blockwise: one accumulation chain per K block (scaled in the general epilogue).
@@ -168,7 +171,7 @@ gemm_status_t choose_swap(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out,
   c->sk_workers = 0;
   c->ws_slots = 1;
   c->group_m = f.group_m ? f.group_m : 16;
-  c->chain_kb = f.chain_kblocks ? f.chain_kblocks : chain_kb_of(kb_elems);
+  c->chain_kb = f.chain_kblocks ? f.chain_kblocks : default_chain(h, kb_elems);
   c->prefetch_kb = f.prefetch_kblocks > 0 ? f.prefetch_kblocks : 0;
   // One tile of A rows, or one wave: every B element is read once, or by every tile of A
   // rows at about the same time, and A by every tile, so B's lines are marked first to be
@@ -273,7 +276,8 @@ gemm_status_t choose_plain(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out
       c->k_blocks >= 8) {
     // 320-column pair tiles (two MMAs per K step) have a cluster-K-split kernel for
     // single-chain slices only
-    const bool try320 = cg == 2 && ceil_div(c->k_blocks, (int64_t)2) <= chain_kb_of(kb_elems);
+    const bool try320 = cg == 2 && !h->short_chains &&
+                        ceil_div(c->k_blocks, (int64_t)2) <= chain_kb_of(kb_elems);
     for (int bn : {128, 256, 320}) {
       if (bn == 320 && !try320) continue;
       const int st = kx_stages(cg, bn, small_a);
@@ -365,7 +369,7 @@ gemm_status_t choose_plain(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out
     c->ws_slots = ceil_div(c->k_blocks, std::max<int64_t>(share, 1)) + 1;
   }
   c->group_m = f.group_m ? f.group_m : 16;
-  c->chain_kb = f.chain_kblocks ? f.chain_kblocks : chain_kb_of(kb_elems);
+  c->chain_kb = f.chain_kblocks ? f.chain_kblocks : default_chain(h, kb_elems);
   if (blockwise) {
     if (f.chain_kblocks > 1 || f.epilogue >= 2) return GEMM_ERR_UNSUPPORTED;
     c->chain_kb = 1;
