@@ -10,7 +10,7 @@ __all__ = ["binding", "roofline", "swizzle"]
 
 
 def __getattr__(name):
-    if name in ("Gemm", "GemmError", "lib", "F16", "BF16", "F32", "GemmConfig"):
+    if name in ("Gemm", "GemmError", "lib", "F16", "BF16", "F32", "GemmConfig", "pair_axes"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

@@ -1,10 +1,12 @@
-"""Run one GEMM shape, or one grouped MoE workload, on the GPU through the C ABI: a
-driver for profilers and sweeps.
+"""Run one GEMM shape, one grouped MoE workload or the projections of a decoding step on
+the GPU through the C ABI: a driver for profilers and sweeps.
 
     python -m dense_gemm_blackwell_02_gb300.run M N K [--in f16|bf16|e4m3|e5m2]
                                                 [--out f16|bf16|f32] [--reps R]
                                                 [--config JSON] [--blockwise BM]
     python -m dense_gemm_blackwell_02_gb300.run --moe NAME [--experts E] [--reps R]
+    python -m dense_gemm_blackwell_02_gb300.run --serve B [--vocab V] [--adapters L] [--rank R]
+                                                [--reps R]
 
 Operands are drawn on the device (uniform [-1, 1], fixed seed), then `gemm_run` (or,
 with --moe, `gemm_run_grouped` over the workload's experts, the first E of them with
@@ -13,6 +15,12 @@ with --moe, `gemm_run_grouped` over the workload's experts, the first E of them 
 one stream.  Prints the kernel configuration the
 library chose and the device status word; exits non-zero if a launch or the status
 reports an error.
+
+--serve B is what a decoding step of B requests asks of the library, attention left out: the
+fused QKV projection with each request's low-rank adapter (`gemm_run_adapters`), rotary
+positions with three axes on the query and key heads in place (`gemm_rotary`), the output
+head's product (`gemm_run`), and penalties, biases and grammar masks on its logits, in place
+(`gemm_adjust_logits`), of which the largest are the next tokens.
 """
 from __future__ import annotations
 
@@ -40,6 +48,53 @@ def _moe_problems(name: str, experts: int, dev, gen):
              torch.empty(m, wl.N, dtype=tout, device=dev)) for m in counts]
 
 
+# The projections of serve(): hidden size, query, key and value heads of 128 (10240 columns).
+HIDDEN, HEADS_Q, HEADS_KV, HEAD_DIM = 8192, 64, 8, 128
+
+
+def serve(g: Gemm, rows: int, vocab: int, adapters: int, rank: int, reps: int, dev, gen) -> dict:
+    """`reps` decoding steps of `rows` requests; returns the last step's tokens."""
+    from .binding import pair_axes
+
+    def normal(*shape, std=1.0):
+        return (torch.randn(*shape, generator=gen, device=dev) * std).bfloat16()
+
+    def ints(lo, hi, *shape):
+        return torch.randint(lo, hi, shape, generator=gen, device=dev, dtype=torch.int32)
+    heads, half = HEADS_Q + HEADS_KV, HEAD_DIM // 2
+    cols = (heads + HEADS_KV) * HEAD_DIM
+    # the model: projections, a pool of adapters, the rotary tables
+    w_qkv, w_out = normal(cols, HIDDEN, std=HIDDEN ** -0.5), normal(vocab, HIDDEN, std=HIDDEN ** -0.5)
+    down, up = normal(adapters, rank, HIDDEN, std=HIDDEN ** -0.5), normal(adapters, cols, rank, std=0.02)
+    angle = (torch.arange(4096, device=dev, dtype=torch.float64)[:, None]
+             * 10000.0 ** (-torch.arange(half, device=dev, dtype=torch.float64) / half))
+    cos, sin = angle.cos().float(), angle.sin().float()
+    axes = pair_axes([half - 2 * (3 * half // 8), 3 * half // 8, 3 * half // 8])
+    # the requests: their adapters (one in nine without), positions, histories, grammars
+    ids, positions = ints(-1, adapters, rows), ints(0, 4096, 3, rows)
+    length = ints(1, 1025, rows).long()
+    start = torch.cat([length.new_zeros(1), length.cumsum(0)])
+    tokens = ints(0, vocab, int(start[-1]))
+    ones = torch.ones(rows, device=dev)
+    mask = ints(-2 ** 31, 2 ** 31 - 1, 2, (vocab + 31) // 32)
+    mask_row = ints(-1, 2, rows)
+    x, hidden = normal(rows, HIDDEN), normal(rows, HIDDEN)
+    qkv = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+    logits = torch.empty(rows, vocab, device=dev)
+    for _ in range(reps):
+        g.run_adapters(x, w_qkv, qkv, down, up, ids)
+        qk = qkv[:, :heads * HEAD_DIM].unflatten(1, (heads, HEAD_DIM))
+        g.rotary(qk, qk, cos, sin, positions, pair_axis=axes)
+        # (attention over qkv and the layers after it would give `hidden`)
+        g.run(hidden, w_out, logits)
+        g.adjust_logits(logits, logits, tokens=tokens, token_start=start,
+                        prompt_len=(length // 2).int(), repetition=1.1 * ones,
+                        frequency=0.1 * ones, presence=0.1 * ones, mask=mask, mask_row=mask_row)
+        chosen = logits.argmax(dim=1)
+    return {"serve": rows, "vocab": vocab, "adapters": adapters, "rank": rank,
+            "finite": bool(torch.isfinite(qkv).all()), "tokens": chosen[:8].tolist()}
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("M", type=int, nargs="?")
@@ -53,16 +108,23 @@ def main(argv=None) -> int:
     ap.add_argument("--experts", type=int, default=0, help="with --moe: only the first E experts")
     ap.add_argument("--blockwise", type=int, default=0,
                     help="FP8 inputs: block scales, one per BM rows of A and 128 of K")
+    ap.add_argument("--serve", type=int, default=0, metavar="B",
+                    help="the projections of a decoding step of B requests")
+    ap.add_argument("--vocab", type=int, default=128256, help="with --serve")
+    ap.add_argument("--adapters", type=int, default=64, help="with --serve: adapters in the pool")
+    ap.add_argument("--rank", type=int, default=16, help="with --serve: the adapters' rank")
     a = ap.parse_args(argv)
-    if a.moe is None and None in (a.M, a.N, a.K):
-        ap.error("M N K are required without --moe")
+    if a.moe is None and not a.serve and None in (a.M, a.N, a.K):
+        ap.error("M N K are required without --moe or --serve")
     dev = torch.device("cuda", 0)
     gen = torch.Generator(device=dev)
     gen.manual_seed(0)
     with Gemm() as g:
         if a.config:
             g.set_config(**json.loads(a.config))
-        if a.moe:
+        if a.serve:
+            shape = serve(g, a.serve, a.vocab, a.adapters, a.rank, a.reps, dev, gen)
+        elif a.moe:
             probs = _moe_problems(a.moe, a.experts, dev, gen)
             for _ in range(a.reps):
                 g.run_grouped(probs)
