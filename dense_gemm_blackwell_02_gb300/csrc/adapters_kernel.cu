@@ -38,6 +38,7 @@ struct TileSlots {
   int16_t slot[kAdapterRows];            // of each row, or -1
   int16_t order[kAdapterRows];           // rows with an adapter, slot after slot
   int16_t start[kAdapterRows + 1];       // of each slot in `order`
+  float scale[kAdapterRows];             // of each slot's adapter
   int32_t warp_firsts[4];
   int32_t slots;
 };
@@ -116,6 +117,8 @@ __device__ void number_slots(TileSlots& ts, const AdapterParams& p, int32_t row0
     if (slot >= 0) ts.order[ts.start[slot] + before] = (int16_t)t;
   }
   __syncthreads();
+  // (read much later, after other barriers)
+  if (t < ts.slots) ts.scale[t] = p.scale ? __ldg(p.scale + ts.adapter[t]) : 1.0f;
 }
 
 // Where a CTA's barriers stand in shared memory.
@@ -348,12 +351,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t quarter = warp & 3u;
     const int32_t row = (int32_t)(quarter * 32 + lane);
     const int32_t slot = ts.slot[row];
+    const float f = slot >= 0 && p.scale ? __ldg(p.scale + ts.adapter[slot]) : 1.0f;
     uint32_t iter = 0;
     for (int32_t u = cta; u < units; u += p.ctas, ++iter) {
       const int32_t g0 = u / splits * per_group, n = min(per_group, ts.slots - g0);
       if (!warp_wait_inl(bars.acc_full(), iter & 1u, ctl, kSiteAdapterAcc)) break;
       tc_fence_after();
-      const float f = slot >= 0 && p.scale ? p.scale[ts.adapter[slot]] : 1.0f;
       for (int32_t j = 0; j < n; ++j) {
         const bool mine = slot == g0 + j;
         if (!__any_sync(0xFFFFFFFFu, mine)) continue;
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int32_t i = r0 + (k * 32 + ((int32_t)threadIdx.x >> 2)) * splits + s;
         const bool on = i < r1;
         const int32_t row = ts.order[min(i, r1 - 1)];
-        const float f = p.scale ? p.scale[ts.id[row]] : 1.0f;
+        const float f = ts.scale[ts.slot[row]];
         const uint32_t src = ring + (uint32_t)(row * (p.rank + 4)) * 4u;
         constexpr int kQuads = kMaxRank / 16;  // of four values, per thread
         float v[kQuads][4];
@@ -423,10 +426,15 @@ __global__ void __launch_bounds__(kThreads, 2)
           v[q][0] = v[q][1] = v[q][2] = v[q][3] = 0.0f;
           if (q * 16 >= p.rank) break;
           if (c < p.rank) {
-            for (int32_t j = 0; j < splits; ++j) {
-              const float4 x = ld_cluster_v4(mapa_shared(src + 4u * (uint32_t)c, (uint32_t)(group * splits + j)));
-              v[q][0] += x.x, v[q][1] += x.y, v[q][2] += x.z, v[q][3] += x.w;
-            }
+            // all slices' sums in flight together (one after the other: 5 us for four)
+            float4 x[8];
+#pragma unroll
+            for (int32_t j = 0; j < 8; ++j)
+              x[j] = j < splits ? ld_cluster_v4(mapa_shared(src + 4u * (uint32_t)c, (uint32_t)(group * splits + j)))
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int32_t j = 0; j < 8; ++j)
+              v[q][0] += x[j].x, v[q][1] += x[j].y, v[q][2] += x[j].z, v[q][3] += x[j].w;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               v[q][e] *= f;

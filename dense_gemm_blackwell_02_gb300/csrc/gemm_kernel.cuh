@@ -743,8 +743,14 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
   // of the preceding kernel; nothing in global memory (A, B, C, the workspace, the
   // status word) is touched before that kernel has completed.  The next kernel may
   // then be scheduled as this one's CTAs exit.
-  grid_dependency_wait();
-  grid_launch_dependents();
+  // (ADAPT: the preceding kernel is the one that prepares the adapters, itself started after
+  // all work before it was complete; what the product reads and writes is not in its hands,
+  // so the product starts beside its tail and each role waits where it first needs u or the
+  // tiles' lists.  The next kernel starts when this one's CTAs exit.)
+  if constexpr (!ADAPT) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer --
@@ -857,6 +863,7 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
         if constexpr (ADAPT) {
           // the tile's adapters: u's two parts, each with the adapter's rows of Up
           const AdapterTile* at = ad.tiles + w.m_blk;
+          grid_dependency_wait();
           const int32_t slots = w.kb1 == p.k_blocks ? __ldg(&at->slots) : 0;
           const int32_t parts = ad.rank <= kBlockK ? 2 : 4;  // two for every 64 values of u
           const CUtensorMap* mapUp = half ? &ad.tmUpHalf : &ad.tmUp;
@@ -1003,6 +1010,7 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
           }
           if constexpr (ADAPT) {
             const AdapterTile* at = ad.tiles + w.m_blk;
+            grid_dependency_wait();
             const int32_t slots = ok && w.kb1 == p.k_blocks ? __ldg(&at->slots) : 0;
             if (slots > 0) {
               const uint32_t slot = iter & (kSlots - 1u), acc_phase = (iter >> kSlotShift) & 1u;
@@ -1230,6 +1238,7 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
       int32_t nchains = base_chains;
       float row_factor = 0.0f;  // (ADAPT) of this thread's row in the adapters' chain
       if constexpr (ADAPT) {
+        grid_dependency_wait();
         if (w.kb1 == p.k_blocks && __ldg(&ad.tiles[w.m_blk].slots) > 0) {
           ++nchains;
           const int32_t m = w.m_blk * kRowsTile + (int32_t)rank * rows_cta + (int32_t)row;

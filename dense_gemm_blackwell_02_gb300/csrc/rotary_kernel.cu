@@ -198,6 +198,12 @@ cudaError_t launch(RotaryParams& p, int sms, cudaStream_t stream) {
   const int64_t spread = ((int64_t)p.tokens * p.heads + 2 * sms - 1) / (2 * sms);
   const int64_t per_cta = std::max<int64_t>(groups, std::min(want, spread));
   p.tile_tokens = (int32_t)std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, per_cta / p.heads));
+  // (four CTAs per SM are resident: not a second round of a few CTAs after a full first one;
+  // 4099 x 16 x 80 binary32 in 684 CTAs 14.2 us, in 586 11.9)
+  const int64_t resident = (int64_t)4 * sms;
+  if ((p.tokens + p.tile_tokens - 1) / p.tile_tokens <= resident * 3 / 2)
+    p.tile_tokens = (int32_t)std::min<int64_t>(
+        kMaxTokens, std::max<int64_t>(p.tile_tokens, (p.tokens + resident - 1) / resident));
   p.shares = (int32_t)((p.heads + per_cta - 1) / per_cta);
   p.share_heads = (p.heads + p.shares - 1) / p.shares;
   p.shares = (p.heads + p.share_heads - 1) / p.share_heads;
