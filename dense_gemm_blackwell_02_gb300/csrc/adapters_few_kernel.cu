@@ -34,6 +34,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = kFewGroup;   // rows of one adapter that are taken together
 constexpr int kUnitRank = 16;      // values of u per unit of few_down
+constexpr int kMaxChecks = 8;      // rows that a CTA of few_down looks at, at most
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
@@ -74,13 +75,18 @@ __device__ __forceinline__ int32_t adapter_of(const AdapterFewParams& p, int32_t
   return a < 0 || a >= p.count ? -1 : a;
 }
 
-template <typename T>
-__device__ __forceinline__ void few_down_unit(const AdapterFewParams& p, int row, int32_t a, bool lists) {
-  const int warp = (int)warp_id(), lane = (int)lane_id();
+// Whether row i begins a group: 16, 32, ... (or no) rows before it name its adapter.
+__device__ __forceinline__ bool begins_group(const AdapterFewParams& p, int row) {
+  const int32_t a = adapter_of(p, row);
   int before = 0;
-  for (int j = lane; j < row; j += 32) before += adapter_of(p, j) == a;
-  before = __reduce_add_sync(0xFFFFFFFFu, before);
-  if (before % kRows != 0) return;
+  for (int j = (int)lane_id(); j < row; j += 32) before += adapter_of(p, j) == a;
+  return __reduce_add_sync(0xFFFFFFFFu, before) % kRows == 0;
+}
+
+template <typename T>
+__device__ __forceinline__ void few_down_unit(const AdapterFewParams& p, int row, bool lists) {
+  const int warp = (int)warp_id(), lane = (int)lane_id();
+  const int32_t a = adapter_of(p, row);
   // lane r of 16: the group's r-th row
   int mine = -1;
   for (int j0 = row & ~31, n = 0; j0 < p.M && n < kRows; j0 += 32) {
@@ -150,21 +156,44 @@ __device__ __forceinline__ void few_down_unit(const AdapterFewParams& p, int row
   }
 }
 
-// A unit of a warp: the group that row i begins (if it begins one), 16 values of u, one K
-// slice of four in a CTA.  Grid: x the row, y the 16 values, z the CTAs' slices.  The groups are listed in the
-// order in which the atomic counter numbers them, which nothing but few_up's schedule
-// depends on.
-template <typename T>
+// A unit: the group that a row begins (if it begins one), 16 values of u, one CTA's share
+// of K.  Grid: x the rows, y the 16 values, z the CTAs' shares.  A CTA looks at `checks`
+// rows, one per warp at a time, because a CTA that only finds that its row begins nothing
+// still costs its launch; the rows are dealt so that neither the first rows of a mixed
+// batch, which all begin groups, nor every 16th of a sorted one fall to the same CTAs.
+// The groups are listed in the order in which the atomic counter
+// numbers them, which nothing but few_up's schedule depends on.
+template <typename T, bool ALONE>
 __global__ void __launch_bounds__(kThreads, 6) few_down_kernel(const AdapterFewParams p) {
   const int warp = (int)warp_id(), lane = (int)lane_id();
-  const int row = (int)blockIdx.x;
-  const int32_t a = adapter_of(p, row);
-  const bool lists = blockIdx.y == 0 && blockIdx.z == 0 && warp == 0;
-  if (lists && lane == 0 && __ldg(p.row_adapter + row) >= p.count)
-    record_bad_index(p.status, kSiteRowAdapter);
-  few_down_unit<T>(p, row, a, lists);
+  const bool lists = blockIdx.y == 0 && blockIdx.z == 0;
+  const auto check = [&](int row, bool reports) {
+    if (reports && lane == 0 && __ldg(p.row_adapter + row) >= p.count)
+      record_bad_index(p.status, kSiteRowAdapter);
+    return begins_group(p, row);
+  };
+  if constexpr (ALONE) {  // checks == 1: every warp looks at it, without a barrier
+    const int row = (int)blockIdx.x;
+    if (check(row, lists && warp == 0)) few_down_unit<T>(p, row, lists && warp == 0);
+  } else {
+    const auto row_of = [](int c) {
+      return c * (int)gridDim.x + ((int)blockIdx.x + 3 * c) % (int)gridDim.x;
+    };
+    __shared__ uint32_t found[kWarps];
+    uint32_t begins = 0;  // bit c: row_of(c) begins a group
+    for (int c = warp; c < p.checks; c += kWarps)
+      if (row_of(c) < p.M && check(row_of(c), lists)) begins |= 1u << c;
+    if (lane == 0) found[warp] = begins;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) begins |= found[w];
+    for (; begins != 0; begins &= begins - 1) {
+      few_down_unit<T>(p, row_of(__ffs((int)begins) - 1), lists && warp == 0);
+      __syncthreads();  // (the next unit writes the same shared memory)
+    }
+  }
   // This grid counts as complete only after the GEMM, so that those after it wait for both.
-  if (row == 0 && lists) grid_dependency_wait();
+  if (blockIdx.x == 0 && lists && warp == 0) grid_dependency_wait();
 }
 
 // 8 or 16 bytes of a row: four or eight values.
@@ -435,13 +464,17 @@ int few_slices(int32_t M, int32_t K, int32_t rank, int32_t count, int sms) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)6 * sms / units, steps / (4 * kWarps), 16}));
 }
 
-cudaError_t launch_adapter_few(const AdapterFewParams& p, int elem_in, int elem_out, int sms,
+cudaError_t launch_adapter_few(AdapterFewParams p, int elem_in, int elem_out, int sms,
                                cudaStream_t stream) {
   const bool f16 = elem_in == kElemF16;
-  const dim3 down((unsigned)p.M, (unsigned)((p.rank + kUnitRank - 1) / kUnitRank),
+  // (half as many units as CTAs, so that few CTAs find two)
+  p.checks = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxChecks, p.M / (2 * max_groups(p))));
+  const dim3 down((unsigned)((p.M + p.checks - 1) / p.checks), (unsigned)((p.rank + kUnitRank - 1) / kUnitRank),
                   (unsigned)p.slices);
   const cudaError_t e =
-      launch(f16 ? few_down_kernel<__half> : few_down_kernel<__nv_bfloat16>, down, p, stream);
+      p.checks == 1
+          ? launch(f16 ? few_down_kernel<__half, true> : few_down_kernel<__nv_bfloat16, true>, down, p, stream)
+          : launch(f16 ? few_down_kernel<__half, false> : few_down_kernel<__nv_bfloat16, false>, down, p, stream);
   if (e != cudaSuccess) return e;
   // As many shares of the columns as are resident at once, of a warp's 32 columns at least.
   const int64_t groups = max_groups(p), resident = (int64_t)up_ctas_per_sm(rank_class(p.rank)) * sms;

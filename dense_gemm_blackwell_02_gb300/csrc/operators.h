@@ -89,6 +89,7 @@ struct AdapterFewParams {
   const int32_t* row_adapter;
   int32_t M, N, K, rank, count;
   int32_t slices;       // partial sums of u (few_slices)
+  int32_t checks;       // rows that a CTA of the first kernel looks at (set by the launch)
   int32_t vec_store;    // 16-byte accesses of eight columns of Y are aligned
   int32_t vec_base;     // rows of base start on 16 bytes
   float* partial;       // M x slices x rank
@@ -99,7 +100,7 @@ struct AdapterFewParams {
   uint32_t* status;
 };
 int few_slices(int32_t M, int32_t K, int32_t rank, int32_t count, int sms);
-cudaError_t launch_adapter_few(const AdapterFewParams& p, int elem_in, int elem_out, int sms,
+cudaError_t launch_adapter_few(AdapterFewParams p, int elem_in, int elem_out, int sms,
                                cudaStream_t stream);
 
 // Many rows (adapters_kernel.cu): u of every row and the tiles' adapters, for the GEMM.
