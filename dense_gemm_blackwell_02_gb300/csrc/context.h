@@ -50,6 +50,7 @@ struct gemm_ctx {
   size_t op_ctr_count = 0;
   gemm_config_t forced = {};
   int32_t short_chains = 0;  // K blocks per accumulation chain where none is forced (0: the default)
+  bool long_slices = false;  // K slices of 16 blocks and more where the choice is free
   gemm_config_t last = {};
   uint64_t wait_limit_ns = 2000000000ull;
   int32_t test_stall = 0;

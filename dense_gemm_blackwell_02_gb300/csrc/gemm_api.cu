@@ -440,6 +440,23 @@ gemm_status_t choose(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int 
   if (st != GEMM_OK || f.swap_ab == 1 || !allow_kx || f.variant || f.block_n || f.splits ||
       f.stages || f.max_ctas || f.chain_kblocks || f.dp_tiles || f.epilogue || f.swap_rows)
     return st;
+  // (`long_slices`) A grid that is cut along K three ways or more and joins through the
+  // workspace: one-CTA 128-column tiles and slices of 16 K blocks, for the join costs more
+  // than the CTAs that finer slices add (16, 128 and 256 rows of A, binary32 results: N 1000
+  // K 2048 8.0, 9.7 and 10.1 us against 16.2, 19.3 and 20.8; N 1000 K 4096 9.6, 11.7 and
+  // 12.2 against 27.6, 30.9 and 33.2; N 2048 K 8192 16.2, 17.7 and 26.9 against 16.8, 18.6
+  // and 28.7; equal at N 4096).
+  if (h->long_slices && !c->kx2 && !c->sk_workers && c->dp_tiles == 0 && c->splits >= 3) {
+    const int64_t tiles = ceil_div(M, (int64_t)kBlockM) * ceil_div(N, (int64_t)128);
+    const gemm_config_t asked = h->forced;
+    h->forced.variant = 1;
+    h->forced.block_n = 128;
+    h->forced.splits =
+        (int32_t)std::max<int64_t>(1, std::min<int64_t>({h->sms / tiles, c->k_blocks / 16, 8}));
+    st = choose_plain(h, M, N, K, out, kb_elems, blockwise, allow_kx, c);
+    h->forced = asked;
+    return st;
+  }
   // The swapped tiling in place of plain one-CTA tiles (17..128 rows of A, K of two
   // accumulation chains or more) that leave a quarter of the SMs idle, with at least 96
   // rows of B per CTA, so that B's rows stay most of each stage next to the 64 rows of A,
@@ -682,6 +699,16 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
     h->forced.block_n = 256;
     h->forced.epilogue = 1;
     st = choose(h, M, N, K, out, kBlockK, false, false, &ch);
+    // A grid cut along K: every slice of a 256 x 256 tile passes 256 KB through the
+    // workspace, so slices of some 40 K blocks on at most two thirds of the pairs (rank 16, four
+    // adapters: 513 x 1000 x 2048 whole 18.6 us, two slices 23.8, six, which would fill the
+    // pairs, 34.4; 600 x 1000 x 4096 27.3, 25.8, 37.5; 600 x 1000 x 8192 44.8, 33.9, 43.8;
+    // 2000 x 704 x 6016 47.7 and 42.1, three slices 43.1; 1024 x 2048 x 8192 45.6 and 52.1).
+    if (st == GEMM_OK && !asked.splits && ch.dp_tiles == 0 && ch.splits > 1) {
+      h->forced.splits = (int32_t)std::max<int64_t>(
+          1, std::min<int64_t>(h->sms / (3 * ch.tiles), (ch.k_blocks + 20) / 40));
+      st = choose(h, M, N, K, out, kBlockK, false, false, &ch);
+    }
     h->forced = asked;
   } else {
     st = choose(h, M, N, K, out, fp8 ? 2 * kBlockK : kBlockK, bs != nullptr, !fp8 && !fused && !bs, &ch);

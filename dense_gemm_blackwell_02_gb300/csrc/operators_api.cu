@@ -52,16 +52,34 @@ gemm_status_t ensure_scratch(gemm_ctx* h, size_t bytes, size_t counters) {
   return GEMM_OK;
 }
 
-// Binary32 results: accumulation chains of K 256 in the products of a scope.  The tensor
-// cores' error grows with a chain's length; at the default K 4096 it was 1.2e-6 of the result
+// What the shared product of a call takes in place of gemm_run's choices.  Binary32 results:
+// accumulation chains of K 256.  The tensor cores' error grows with a chain's length; at the default K 4096 it was 1.2e-6 of the result
 // (relative Frobenius), where sums in binary32 have 2.4e-7.  16-bit results round by 1000
-// times that.
+// times that.  And K slices of 16 blocks (in choose()).
 constexpr int kShortChain = 4;  // K blocks
-struct ShortChains {
+struct ProductRules {
   gemm_ctx* h;
-  ShortChains(gemm_ctx* h_, bool on) : h(h_) { h->short_chains = on ? kShortChain : 0; }
-  ~ShortChains() { h->short_chains = 0; }
+  ProductRules(gemm_ctx* h_, bool f32) : h(h_) {
+    h->short_chains = f32 ? kShortChain : 0;
+    h->long_slices = true;
+  }
+  ~ProductRules() { h->short_chains = 0, h->long_slices = false; }
 };
+
+// More than 128 rows and a small pool beside a wide product: its 256 x 256 tiles occupy more
+// than half of the CTA pairs without K slices, and at most eight adapters' u and terms cost
+// them less than the binary32 product's way through memory costs the kernels for few rows
+// (those kernels against the tiles, us: 256 x 10240 x 8192, 2 adapters of rank 16 53 and 45,
+// of rank 64 61 and 46, 8 of rank 64 63 and 51, 32 of rank 16 58 and 62; 512 x 10240 x 8192,
+// 4 of rank 128 112 and 77; 256 x 14336 x 4096, 8 of rank 16 38 and 33; with K slices,
+// 256 x 8192 x 8192, 8 of rank 16 39 and 42; 256 x 4096 x 4096 21 and 35).
+bool prefers_tiles(const gemm_ctx* h, int64_t M, int64_t N, const gemm_adapters_t* ad) {
+  const gemm_config_t& f = h->forced;
+  if (f.variant || f.block_n || f.splits || f.stages || f.epilogue || f.swap_ab || f.max_ctas)
+    return false;
+  return M > kAdapterRows && ad->count <= 8 && ad->count * ad->rank <= 512 &&
+         4 * ceil_div(M, 256) * ceil_div(N, 256) > h->sms;
+}
 
 gemm_status_t launched(gemm_ctx* h, cudaError_t e) {
   h->last_cuda = e;
@@ -99,8 +117,8 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
   const bool base_in_y = dtype_out == GEMM_F32;
-  const ShortChains chains(h, dtype_out == GEMM_F32);
-  if (M <= kFewRows) {
+  const ProductRules rules(h, dtype_out == GEMM_F32);
+  if (M <= kFewRows && !prefers_tiles(h, M, N, ad)) {
     AdapterFewParams f;
     std::memset(&f, 0, sizeof(f));
     f.slices = few_slices((int32_t)M, (int32_t)K, ad->rank, ad->count, h->sms);

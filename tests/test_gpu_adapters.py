@@ -124,6 +124,27 @@ def test_adapters_against_the_formula(g, M, N, K, R, L, din, dout, ids):
     _check(Y, want, tau, dout)
 
 
+# Where the paths meet: a small pool beside a wide product (tiles from 129 rows on), the same
+# rows with one adapter more, sorted and mixed batches of few groups, products cut along K.
+@pytest.mark.parametrize("M,N,K,R,L,din,dout,ids", [
+    (129, 10248, 136, 24, 8, BF16, BF16, "mixed"),
+    (300, 5130, 328, 64, 8, BF16, F32, "runs"),
+    (300, 5130, 328, 64, 9, BF16, F32, "runs"),
+    (512, 5128, 200, 128, 4, F16, F16, "mixed"),
+    (512, 264, 512, 16, 3, BF16, BF16, "runs"),
+    (511, 136, 520, 40, 2, F16, BF16, "mixed"),
+    (385, 130, 264, 16, 1, BF16, F32, "one"),
+    (40, 600, 4096, 32, 40, BF16, F32, "mixed"),
+    (90, 130, 16384, 16, 5, BF16, BF16, "mixed"),
+    (600, 520, 4096, 16, 4, BF16, BF16, "mixed"),
+    (520, 200, 12288, 32, 3, F16, F32, "runs"),
+])
+def test_adapters_around_the_choice_of_path(g, M, N, K, R, L, din, dout, ids):
+    t = _inputs(M, N, K, R, L, TD[din], ids, seed=13 * M + N + K)
+    want, tau = _expect(t)
+    _check(_run(g, t, TD[dout]), want, tau, dout)
+
+
 def test_every_rank(g):
     for R in range(8, 129, 8):
         t = _inputs(150, 264, 520, R, 6, torch.bfloat16, "mixed", seed=R, scale=False)
