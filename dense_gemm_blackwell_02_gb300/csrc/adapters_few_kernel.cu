@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
   __shared__ alignas(16) T hi[kRows * kPitch];
   __shared__ alignas(16) T lo[kRows * kPitch];
   __shared__ float row_scale[kRows];
+  __shared__ float turn[kWarps][8][33];
   const int tid = (int)threadIdx.x, warp = (int)warp_id(), lane = (int)lane_id();
   const int g = lane >> 2, t = lane & 3;
   grid_dependency_wait();
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
     };
     auto load_base = [&](int qq, int row, float (&dst)[8]) {
       const int n = qq * 32 + 8 * t;
-      const float* src = p.base + (int64_t)max(row, 0) * p.N + n;
+      const float* src = p.base + (int64_t)max(row, 0) * p.base_pitch + n;
 #pragma unroll
       for (int k = 0; k < 8; ++k) dst[k] = 0.0f;
       if (row < 0 || qq >= groups) return;
@@ -280,15 +281,23 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
     };
     auto store = [&](int qq, int row, const float (&src)[8]) {
       const int n = qq * 32 + 8 * t;
-      if (row < 0) return;
-      TO* y = static_cast<TO*>(p.Y) + (int64_t)row * p.N + n;
-      if (p.vec_store && n + 8 <= p.N) {
-        store_f32<TO, 8>(y, src);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (n + k < p.N) y[k] = from_f32<TO>(src[k]);
+      TO* y = static_cast<TO*>(p.Y);
+      if (p.vec_store) {
+        if (row >= 0 && n < p.N) store_f32<TO, 8>(y + (int64_t)row * p.N + n, src);
+        return;
       }
+      // Y's rows begin anywhere: through shared memory, so that a store of the warp writes
+      // 32 neighbouring values of a row rather than one of eight rows' every eighth
+#pragma unroll
+      for (int k = 0; k < 8; ++k) turn[warp][g][8 * t + k] = src[k];
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int to = __shfl_sync(0xFFFFFFFFu, row, 4 * r);
+        if (to >= 0 && qq * 32 + lane < p.N)
+          y[(int64_t)to * p.N + qq * 32 + lane] = from_f32<TO>(turn[warp][r][lane]);
+      }
+      __syncwarp();
     };
     load_up(q, b);
     load_base(q, row0, o);

@@ -50,6 +50,9 @@ struct gemm_ctx {
   size_t op_ctr_count = 0;
   gemm_config_t forced = {};
   int32_t short_chains = 0;  // K blocks per accumulation chain where none is forced (0: the default)
+  // elements per row of C where not N: a whole number of 16 bytes; C is then written by TMA
+  // alone (no swapped tiling, no 320-column tiles, nothing forced)
+  int64_t c_pitch = 0;
   bool long_slices = false;  // K slices of 16 blocks and more where the choice is free
   gemm_config_t last = {};
   uint64_t wait_limit_ns = 2000000000ull;

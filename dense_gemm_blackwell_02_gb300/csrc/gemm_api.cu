@@ -276,7 +276,7 @@ gemm_status_t choose_plain(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out
       c->k_blocks >= 8) {
     // 320-column pair tiles (two MMAs per K step) have a cluster-K-split kernel for
     // single-chain slices only
-    const bool try320 = cg == 2 && !h->short_chains &&
+    const bool try320 = cg == 2 && !h->short_chains && !h->c_pitch &&
                         ceil_div(c->k_blocks, (int64_t)2) <= chain_kb_of(kb_elems);
     for (int bn : {128, 256, 320}) {
       if (bn == 320 && !try320) continue;
@@ -471,7 +471,7 @@ gemm_status_t choose(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int 
   // rows the plain pair tiles keep up with it (256 x 8192 x 4096, unsplit 128-column
   // tiles: 19.5 against 19.8; 256 x 8192 x 8192, the cluster K split: 31.1 against 32.2).
   Choice sw;
-  if (M <= 16 || M > kBlockM || c->k_blocks < 2 * chain_kb_of(kb_elems) ||
+  if (h->c_pitch || M <= 16 || M > kBlockM || c->k_blocks < 2 * chain_kb_of(kb_elems) ||
       4 * (int64_t)c->grid > 3 * (int64_t)h->sms)
     return st;
   if (choose_swap(h, M, N, K, out, kb_elems, &sw) != GEMM_OK || sw.swap_rows < 96)
@@ -735,7 +735,9 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
   s.staged = !ch.kx2 && !ch.swap && !s.fused && !ad && s.kind == 0 && !ch.one_chain &&
              ((ch.splits > 1 && !ch.half_tail) || ch.sk_workers);
   s.stream = stream;
-  const bool c_tma = reinterpret_cast<uintptr_t>(C) % 16 == 0 && ((size_t)N * osz) % 16 == 0;
+  // (a pitch makes C's rows 16-byte aligned; TMA stores then write its rows' ends too, as 0)
+  const int64_t c_cols = h->c_pitch ? h->c_pitch : N;
+  const bool c_tma = reinterpret_cast<uintptr_t>(C) % 16 == 0 && ((size_t)c_cols * osz) % 16 == 0;
   // A single one-CTA row tile of M < 128 rows loads A as an M-row box: the stage's
   // rows M..127 are never written and only feed accumulator rows that are never
   // stored.  (A 128-row box over fewer than 8 rows of A ran up to 1.5x slower on the
@@ -752,7 +754,7 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
   } else if (!make_map(h, A, M, K, dtype_in, a_box, &s.tmA) ||
       !make_map(h, B, N, K, dtype_in, ch.bn == 320 ? 128 : ch.bn / ch.variant, &s.tmB) ||
       (ch.half_tail && !make_map(h, B, N, K, dtype_in, ch.bn / ch.variant / 2, &s.tmB2)) ||
-      (c_tma && !make_map(h, C, M, N, dtype_out, 32, &s.tmC)))
+      (c_tma && !make_map(h, C, M, c_cols, dtype_out, 32, &s.tmC)))
     return GEMM_ERR_CUDA;
   if (ch.swap) {
   } else if (ch.bn == 320) {

@@ -1734,12 +1734,16 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
         }
       } else {
         // (row stores: the transposed form of the single-chain epilogue raised this
-        // epilogue's register spills)
+        // epilogue's register spills; with adapters it pays all the same, 2883 x 2653 x 3968
+        // in fp16 68 us against 135)
         const int32_t m = m0 + (int32_t)row;
 #pragma unroll
         for (int pc = 0; pc < kPieces; ++pc) {
           if constexpr (GROUPED)
             store_row_to<OUT>(gd->C, gd->M, gd->N, gd->vec_store, m, n_half + 32 * pc, acc + 32 * pc);
+          else if constexpr (ADAPT)
+            store_piece_rows<OUT>(p.C, p.M, p.N, m0 + (int32_t)(q * 32u), n_half + 32 * pc,
+                                  acc + 32 * pc, staging);
           else
             store_row_direct<OUT>(p, m, n_half + 32 * pc, acc + 32 * pc);
         }

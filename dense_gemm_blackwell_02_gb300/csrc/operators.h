@@ -88,6 +88,7 @@ struct AdapterFewParams {
   const float* scale;   // count, or nullptr
   const int32_t* row_adapter;
   int32_t M, N, K, rank, count;
+  int64_t base_pitch;   // values per row of base
   int32_t slices;       // partial sums of u (few_slices)
   int32_t checks;       // rows that a CTA of the first kernel looks at (set by the launch)
   int32_t vec_store;    // 16-byte accesses of eight columns of Y are aligned

@@ -63,8 +63,14 @@ struct ProductRules {
     h->short_chains = f32 ? kShortChain : 0;
     h->long_slices = true;
   }
-  ~ProductRules() { h->short_chains = 0, h->long_slices = false; }
+  ~ProductRules() { h->short_chains = 0, h->long_slices = false, h->c_pitch = 0; }
 };
+
+bool nothing_forced(const gemm_ctx* h) {
+  const gemm_config_t& f = h->forced;
+  return !f.variant && !f.block_n && !f.splits && !f.stages && !f.epilogue && !f.swap_ab &&
+         !f.max_ctas;
+}
 
 // More than 128 rows and a small pool beside a wide product: its 256 x 256 tiles occupy more
 // than half of the CTA pairs without K slices, and at most eight adapters' u and terms cost
@@ -74,10 +80,7 @@ struct ProductRules {
 // 4 of rank 128 112 and 77; 256 x 14336 x 4096, 8 of rank 16 38 and 33; with K slices,
 // 256 x 8192 x 8192, 8 of rank 16 39 and 42; 256 x 4096 x 4096 21 and 35).
 bool prefers_tiles(const gemm_ctx* h, int64_t M, int64_t N, const gemm_adapters_t* ad) {
-  const gemm_config_t& f = h->forced;
-  if (f.variant || f.block_n || f.splits || f.stages || f.epilogue || f.swap_ab || f.max_ctas)
-    return false;
-  return M > kAdapterRows && ad->count <= 8 && ad->count * ad->rank <= 512 &&
+  return nothing_forced(h) && M > kAdapterRows && ad->count <= 8 && ad->count * ad->rank <= 512 &&
          4 * ceil_div(M, 256) * ceil_div(N, 256) > h->sms;
 }
 
@@ -116,19 +119,24 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     return GEMM_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
-  const bool base_in_y = dtype_out == GEMM_F32;
   const ProductRules rules(h, dtype_out == GEMM_F32);
   if (M <= kFewRows && !prefers_tiles(h, M, N, ad)) {
     AdapterFewParams f;
     std::memset(&f, 0, sizeof(f));
     f.slices = few_slices((int32_t)M, (int32_t)K, ad->rank, ad->count, h->sms);
-    const size_t base_bytes = base_in_y ? 0 : round_up((size_t)M * N * sizeof(float));
+    // The binary32 product lies in Y where Y can hold it, else in the scratch: rows of
+    // 16-byte multiples, which TMA writes and few_up reads 16 bytes at a time (148 x 9302 x
+    // 2056, rank 128, binary32: 41 us against 52.5).
+    const bool base_in_y = dtype_out == GEMM_F32 && (N % 4 == 0 || !nothing_forced(h));
+    f.base_pitch = base_in_y || !nothing_forced(h) ? N : ceil_div(N, 4) * 4;
+    const size_t base_bytes = base_in_y ? 0 : round_up((size_t)M * f.base_pitch * sizeof(float));
     const size_t part_bytes = round_up((size_t)M * f.slices * ad->rank * sizeof(float));
     gemm_status_t st = ensure_scratch(
         h, base_bytes + part_bytes + (size_t)M * sizeof(FewGroup), 2);
     if (st != GEMM_OK) return st;
     char* scratch = static_cast<char*>(h->d_op);
     void* base = base_in_y ? Y : scratch;
+    if (f.base_pitch != N) h->c_pitch = f.base_pitch;
     st = gemm_run(h, X, W, base, M, N, K, dtype_in, GEMM_F32, stream_);
     if (st != GEMM_OK) return st;
     f.X = X;
@@ -142,7 +150,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     f.rank = ad->rank;
     f.count = ad->count;
     f.vec_store = aligned(Y, 16) && N % 8 == 0;
-    f.vec_base = aligned(base, 16) && N % 4 == 0;
+    f.vec_base = aligned(base, 16) && f.base_pitch % 4 == 0;
     f.partial = reinterpret_cast<float*>(scratch + base_bytes);
     f.groups = reinterpret_cast<FewGroup*>(scratch + base_bytes + part_bytes);
     f.counts = h->d_op_ctr;

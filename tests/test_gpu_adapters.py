@@ -138,6 +138,14 @@ def test_adapters_against_the_formula(g, M, N, K, R, L, din, dout, ids):
     (90, 130, 16384, 16, 5, BF16, BF16, "mixed"),
     (600, 520, 4096, 16, 4, BF16, BF16, "mixed"),
     (520, 200, 12288, 32, 3, F16, F32, "runs"),
+    # rows of Y that begin at any 2 or 4 bytes, one row, tiles of the product cut in two
+    (1, 1003, 2048, 16, 3, BF16, F32, "one"),
+    (1, 30, 264, 16, 3, F16, F16, "one"),
+    (17, 4099, 4096, 64, 6, BF16, F32, "mixed"),
+    (140, 10241, 8192, 16, 20, F16, F32, "mixed"),
+    (64, 6145, 8192, 128, 9, BF16, BF16, "runs"),
+    (500, 2306, 1544, 32, 1, BF16, F16, "one"),
+    (2600, 2653, 200, 16, 17, F16, F16, "runs"),
 ])
 def test_adapters_around_the_choice_of_path(g, M, N, K, R, L, din, dout, ids):
     t = _inputs(M, N, K, R, L, TD[din], ids, seed=13 * M + N + K)
