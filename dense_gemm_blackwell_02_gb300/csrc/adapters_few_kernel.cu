@@ -463,12 +463,16 @@ int64_t max_groups(const AdapterFewParams& p) {
 
 }  // namespace
 
-int few_slices(int32_t M, int32_t K, int32_t rank, int32_t count, int sms) {
+int64_t few_down_rows(int32_t M, int32_t rank, int32_t count) {
   AdapterFewParams p = {};
   p.M = M;
   p.count = count;
+  return max_groups(p) * ((rank + kUnitRank - 1) / kUnitRank * kUnitRank);
+}
+
+int few_slices(int32_t M, int32_t K, int32_t rank, int32_t count, int sms) {
   // As many K slices as give every SM its six CTAs, a warp at least four steps of 32.
-  const int64_t units = max_groups(p) * ((rank + kUnitRank - 1) / kUnitRank);
+  const int64_t units = few_down_rows(M, rank, count) / kUnitRank;
   const int64_t steps = ((int64_t)K + 31) / 32;
   return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)6 * sms / units, steps / (4 * kWarps), 16}));
 }

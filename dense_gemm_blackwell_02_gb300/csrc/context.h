@@ -53,7 +53,8 @@ struct gemm_ctx {
   // elements per row of C where not N: a whole number of 16 bytes; C is then written by TMA
   // alone (no swapped tiling, no 320-column tiles, nothing forced)
   int64_t c_pitch = 0;
-  bool long_slices = false;  // K slices of 16 blocks and more where the choice is free
+  // rows of K values that another kernel streams beside the product (0: none does)
+  int64_t beside_rows = 0;
   gemm_config_t last = {};
   uint64_t wait_limit_ns = 2000000000ull;
   int32_t test_stall = 0;

@@ -429,6 +429,63 @@ gemm_status_t choose_plain(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out
   return GEMM_OK;
 }
 
+// For a product that runs beside a kernel which streams beside_rows rows of K values of its
+// own (the first kernel of the adapters for few rows), in place of choose_plain's choice c:
+//
+// A grid that is cut along K three ways or more and joins through the workspace: one-CTA
+// 128-column tiles and slices of 16 K blocks, for the join costs more than the CTAs that
+// finer slices add (16, 128 and 256 rows of A, binary32 results: N 1000 K 2048 8.0, 9.7 and
+// 10.1 us against 16.2, 19.3 and 20.8; N 1000 K 4096 9.6, 11.7 and 12.2 against 27.6, 30.9
+// and 33.2; N 2048 K 8192 16.2, 17.7 and 26.9 against 16.8, 18.6 and 28.7; equal at N 4096).
+//
+// A grid that takes more than the product's share of the SMs, by the rows that either kernel
+// streams: the largest grid within that share, else the smallest that is a quarter of the
+// SMs.  The other kernel has room for one CTA next
+// to one of the product's, for six on an SM of its own, and both are bound by how much they
+// keep in flight (with 64 adapters of rank 64, 256 x 8192 x 8192: 64 CTAs 65 us against 88
+// for 128; 256 x 4096 x 4096 30 against 45; with 16 of rank 64, 256 x 8192 x 8192: 104 CTAs
+// 48 against 58; with 64 of rank 16, 256 x 10240 x 8192: 128 CTAs 54 against 62 for
+// stream-K on 152).
+void choose_beside(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int kb_elems, Choice* c) {
+  const gemm_config_t asked = h->forced;
+  const auto forced = [&](int variant, int bn, int splits, int epilogue, Choice* to) {
+    h->forced.variant = variant;
+    h->forced.block_n = bn;
+    h->forced.splits = splits;
+    h->forced.epilogue = epilogue;
+    const gemm_status_t st = choose_plain(h, M, N, K, out, kb_elems, false, true, to);
+    h->forced = asked;
+    return st == GEMM_OK;
+  };
+  const int64_t narrow = ceil_div(M, (int64_t)kBlockM) * ceil_div(N, (int64_t)128);
+  if (!c->kx2 && !c->sk_workers && c->dp_tiles == 0 && c->splits >= 3) {
+    const int64_t s = std::min<int64_t>({h->sms / narrow, c->k_blocks / 16, 8});
+    forced(1, 128, (int)std::max<int64_t>(1, s), 0, c);
+  }
+  const int64_t share = h->sms * N / (N + h->beside_rows);
+  if (c->grid <= share) return;
+  const int v = M > kBlockM ? 2 : 1;
+  const struct {
+    int bn, splits, epilogue;
+  } smaller[] = {{320, 2, 3}, {256, 2, 3}, {128, 1, 0}, {256, 1, 0}, {128, 3, 0}, {128, 2, 0}};
+  int64_t best = 0, least = c->grid;
+  Choice fallback = *c;
+  for (const auto& t : smaller) {
+    if (t.bn == 320 && (v == 1 || h->short_chains || h->c_pitch)) continue;
+    if (v == 2 && t.bn == 128 && t.splits > 1) continue;
+    Choice to;
+    if (!forced(v, t.bn, t.splits, t.epilogue, &to) || to.units * v != to.grid) continue;
+    if (to.grid <= share && to.grid > best) {
+      best = to.grid;
+      *c = to;
+    } else if (to.grid > share && to.grid < least && 4 * to.grid >= h->sms) {
+      least = to.grid;
+      fallback = to;
+    }
+  }
+  if (best == 0) *c = fallback;
+}
+
 gemm_status_t choose(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int kb_elems,
                      bool blockwise, bool allow_kx, Choice* c) {
   const gemm_config_t& f = h->forced;
@@ -440,22 +497,9 @@ gemm_status_t choose(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int 
   if (st != GEMM_OK || f.swap_ab == 1 || !allow_kx || f.variant || f.block_n || f.splits ||
       f.stages || f.max_ctas || f.chain_kblocks || f.dp_tiles || f.epilogue || f.swap_rows)
     return st;
-  // (`long_slices`) A grid that is cut along K three ways or more and joins through the
-  // workspace: one-CTA 128-column tiles and slices of 16 K blocks, for the join costs more
-  // than the CTAs that finer slices add (16, 128 and 256 rows of A, binary32 results: N 1000
-  // K 2048 8.0, 9.7 and 10.1 us against 16.2, 19.3 and 20.8; N 1000 K 4096 9.6, 11.7 and
-  // 12.2 against 27.6, 30.9 and 33.2; N 2048 K 8192 16.2, 17.7 and 26.9 against 16.8, 18.6
-  // and 28.7; equal at N 4096).
-  if (h->long_slices && !c->kx2 && !c->sk_workers && c->dp_tiles == 0 && c->splits >= 3) {
-    const int64_t tiles = ceil_div(M, (int64_t)kBlockM) * ceil_div(N, (int64_t)128);
-    const gemm_config_t asked = h->forced;
-    h->forced.variant = 1;
-    h->forced.block_n = 128;
-    h->forced.splits =
-        (int32_t)std::max<int64_t>(1, std::min<int64_t>({h->sms / tiles, c->k_blocks / 16, 8}));
-    st = choose_plain(h, M, N, K, out, kb_elems, blockwise, allow_kx, c);
-    h->forced = asked;
-    return st;
+  if (h->beside_rows) {
+    choose_beside(h, M, N, K, out, kb_elems, c);
+    return GEMM_OK;
   }
   // The swapped tiling in place of plain one-CTA tiles (17..128 rows of A, K of two
   // accumulation chains or more) that leave a quarter of the SMs idle, with at least 96

@@ -101,6 +101,8 @@ struct AdapterFewParams {
   uint32_t* status;
 };
 int few_slices(int32_t M, int32_t K, int32_t rank, int32_t count, int sms);
+// Rows of Down that the first kernel streams, at most.
+int64_t few_down_rows(int32_t M, int32_t rank, int32_t count);
 cudaError_t launch_adapter_few(AdapterFewParams p, int elem_in, int elem_out, int sms,
                                cudaStream_t stream);
 

@@ -55,15 +55,14 @@ gemm_status_t ensure_scratch(gemm_ctx* h, size_t bytes, size_t counters) {
 // What the shared product of a call takes in place of gemm_run's choices.  Binary32 results:
 // accumulation chains of K 256.  The tensor cores' error grows with a chain's length; at the default K 4096 it was 1.2e-6 of the result
 // (relative Frobenius), where sums in binary32 have 2.4e-7.  16-bit results round by 1000
-// times that.  And K slices of 16 blocks (in choose()).
+// times that.
 constexpr int kShortChain = 4;  // K blocks
 struct ProductRules {
   gemm_ctx* h;
   ProductRules(gemm_ctx* h_, bool f32) : h(h_) {
     h->short_chains = f32 ? kShortChain : 0;
-    h->long_slices = true;
   }
-  ~ProductRules() { h->short_chains = 0, h->long_slices = false, h->c_pitch = 0; }
+  ~ProductRules() { h->short_chains = 0, h->beside_rows = 0, h->c_pitch = 0; }
 };
 
 bool nothing_forced(const gemm_ctx* h) {
@@ -136,6 +135,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     if (st != GEMM_OK) return st;
     char* scratch = static_cast<char*>(h->d_op);
     void* base = base_in_y ? Y : scratch;
+    h->beside_rows = few_down_rows((int32_t)M, ad->rank, ad->count);
     if (f.base_pitch != N) h->c_pitch = f.base_pitch;
     st = gemm_run(h, X, W, base, M, N, K, dtype_in, GEMM_F32, stream_);
     if (st != GEMM_OK) return st;
