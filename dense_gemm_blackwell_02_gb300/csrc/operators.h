@@ -74,6 +74,8 @@ constexpr int kAdapterCols = 128;   // columns of Down . X per group of adapters
 
 // A batch of few rows (adapters_few_kernel.cu), queued right after the shared product.
 constexpr int kFewRows = 512;
+constexpr int kFewRowsLargePool = 2048;  // of a pool of more than kLargePool adapters
+constexpr int kLargePool = 32;
 constexpr int kFewGroup = 16;  // rows of one adapter that are taken together
 struct FewGroup {
   int32_t adapter;          // -1: none
@@ -82,7 +84,7 @@ struct FewGroup {
   int32_t pad[14];          // 128 bytes
 };
 struct AdapterFewParams {
-  const void* X;        // M x K, M <= kFewRows
+  const void* X;        // M x K, M <= kFewRowsLargePool
   const void* down;     // count x rank x K
   const void* up;       // count x N x rank
   const float* scale;   // count, or nullptr

@@ -71,16 +71,23 @@ bool nothing_forced(const gemm_ctx* h) {
          !f.max_ctas;
 }
 
-// More than 128 rows and a small pool beside a wide product: its 256 x 256 tiles occupy more
-// than half of the CTA pairs without K slices, and at most eight adapters' u and terms cost
-// them less than the binary32 product's way through memory costs the kernels for few rows
-// (those kernels against the tiles, us: 256 x 10240 x 8192, 2 adapters of rank 16 53 and 45,
-// of rank 64 61 and 46, 8 of rank 64 63 and 51, 32 of rank 16 58 and 62; 512 x 10240 x 8192,
-// 4 of rank 128 112 and 77; 256 x 14336 x 4096, 8 of rank 16 38 and 33; with K slices,
-// 256 x 8192 x 8192, 8 of rank 16 39 and 42; 256 x 4096 x 4096 21 and 35).
-bool prefers_tiles(const gemm_ctx* h, int64_t M, int64_t N, const gemm_adapters_t* ad) {
-  return nothing_forced(h) && M > kAdapterRows && ad->count <= 8 && ad->count * ad->rank <= 512 &&
-         4 * ceil_div(M, 256) * ceil_div(N, 256) > h->sms;
+// Whether the kernels for few rows serve the call, or 256 x 256 tiles with the adapters' term
+// in their last MMAs.  The first cost about the same however the rows are mixed, but their
+// binary32 product goes through memory; the second's cost grows with the adapters that a
+// tile's rows name, which the host does not see.  Up to 512 rows the first (256 x 4096 x
+// 4096, 8 adapters of rank 16, us: 20 against 28 for the tiles; 256 x 8192 x 8192 39 and 48;
+// 512 x 4096 x 4096, 16 of rank 64, mixed 36 and 52), except more than 128 rows and a small
+// pool beside a product whose tiles occupy more than half of the CTA pairs without K slices
+// (256 x 10240 x 8192, 2 of rank 64 56 and 46, 4 of rank 128 59 and 51, 8 of rank 16 48 and
+// 48; 512 x 10240 x 8192, 8 of rank 64 97 and 78; 256 x 14336 x 4096, 8 of rank 16 37 and
+// 33).  Up to 2048 rows the first for a large pool (1024 x 8192 x 8192, 64 of rank 16, mixed
+// 126 and 214, sorted 112 and 119; 64 of rank 64 221 and 336, 183 and 145; 1024 x 2048 x
+// 2048, 64 of rank 16 25 and 66, 25 and 27), and for a small one the second (24 of rank 64
+// 175 and 186, 172 and 119).
+bool takes_few_rows(const gemm_ctx* h, int64_t M, int64_t N, const gemm_adapters_t* ad) {
+  if (M > kFewRows) return M <= kFewRowsLargePool && ad->count > kLargePool;
+  const bool wide = M > kAdapterRows && 4 * ceil_div(M, 256) * ceil_div(N, 256) > h->sms;
+  return !(wide && nothing_forced(h) && ad->count <= 8 && ad->count * ad->rank <= 512);
 }
 
 gemm_status_t launched(gemm_ctx* h, cudaError_t e) {
@@ -119,7 +126,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
   const ProductRules rules(h, dtype_out == GEMM_F32);
-  if (M <= kFewRows && !prefers_tiles(h, M, N, ad)) {
+  if (takes_few_rows(h, M, N, ad)) {
     AdapterFewParams f;
     std::memset(&f, 0, sizeof(f));
     f.slices = few_slices((int32_t)M, (int32_t)K, ad->rank, ad->count, h->sms);

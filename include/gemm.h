@@ -458,8 +458,9 @@ typedef struct {
  *                          not 16-byte aligned, scale or row_adapter not 4-byte aligned,
  *                          count * rank or count * N above INT32_MAX.
  * K == 0 writes Y = 0.  gemm_set_config applies to the shared product: for more than 512
- * rows it runs on CTA pairs of 256 columns with the general epilogue, and a forced variant,
- * block_n, epilogue or swap_ab that contradicts this gives GEMM_ERR_UNSUPPORTED. */
+ * rows (2048 with a pool of more than 32 adapters) it runs on CTA pairs of 256 columns with
+ * the general epilogue, and a forced variant, block_n, epilogue or swap_ab that contradicts
+ * this gives GEMM_ERR_UNSUPPORTED. */
 gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, void* Y, int64_t M,
                                 int64_t N, int64_t K, gemm_dtype_t dtype_in,
                                 gemm_dtype_t dtype_out, const gemm_adapters_t* adapters,

@@ -146,6 +146,13 @@ def test_adapters_against_the_formula(g, M, N, K, R, L, din, dout, ids):
     (64, 6145, 8192, 128, 9, BF16, BF16, "runs"),
     (500, 2306, 1544, 32, 1, BF16, F16, "one"),
     (2600, 2653, 200, 16, 17, F16, F16, "runs"),
+    # more rows of a large pool, and past them tiles with more adapters than one group holds
+    (513, 264, 520, 16, 33, BF16, BF16, "runs"),
+    (2048, 130, 264, 64, 40, F16, F32, "mixed"),
+    (1500, 1001, 136, 8, 700, BF16, BF16, "mixed"),
+    (2049, 300, 4104, 16, 40, BF16, BF16, "mixed"),
+    (2050, 257, 24, 128, 200, F16, BF16, "mixed"),
+    (2100, 513, 1032, 48, 600, BF16, BF16, "mixed"),
 ])
 def test_adapters_around_the_choice_of_path(g, M, N, K, R, L, din, dout, ids):
     t = _inputs(M, N, K, R, L, TD[din], ids, seed=13 * M + N + K)
