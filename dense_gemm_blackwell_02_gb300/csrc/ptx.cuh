@@ -148,15 +148,6 @@ __device__ __forceinline__ void bulk_copy_s2cluster(uint32_t dst, uint32_t src, 
       : "memory");
 }
 
-// Bulk copy of `bytes` (a multiple of 16) of contiguous global memory to this CTA's shared
-// memory; the bytes complete_tx on `bar`.  Both addresses 16-byte aligned.
-__device__ __forceinline__ void bulk_copy_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // shared::cta address -> the same offset in CTA `rank` of the cluster (shared::cluster).
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   uint32_t r;
