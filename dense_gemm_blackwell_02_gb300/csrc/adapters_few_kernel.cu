@@ -9,12 +9,19 @@
 //
 // The rows that name one adapter form groups of 16.  few_down runs beside the GEMM: it is
 // launched after it but waits for it only at its end (programmatic dependent launch; what
-// it reads are the call's inputs, complete when the GEMM started), and it needs what the
-// GEMM leaves of an SM: 80 registers for 128 threads, and 5 KiB of shared memory where the
-// GEMM keeps its staging in the ring (the cluster K split and the swapped tiling of the
-// decode shapes).  A CTA's warps share a K slice of 16 values of a group's u, weights
+// it reads are the call's inputs, complete when the GEMM started).  Next to a CTA of the
+// GEMM an SM has room for one of few_down's (80 registers for 128 threads, 5 KiB of shared
+// memory where the GEMM keeps its staging in the ring), alone for six, so the GEMM's tiling
+// leaves it some SMs.  A CTA's warps share a K slice of 16 values of a group's u, weights
 // straight from global memory into MMA fragments, and leave partial sums for few_up to add
-// in order.
+// in order.  Ahead of the GEMM instead of beside it the whole is slower (64 adapters of
+// rank 16, 256 x 10240 x 8192 67 us against 55; 256 x 1000 x 2048 32 against 15).
+//
+// Measured, bf16 over cold operands, 256 x 10240 x 8192, 64 adapters of rank 16: 55 us, of
+// which the product alone is 40 (168 MB, 4.2 TB/s) and few_up after it 10 (Up's 21 MB from
+// HBM, the binary32 product's 10 MB from L2); few_down's 17 MB cost the product 5.  One row,
+// 8192 x 8192: 32 us, the product alone 26.  Looking further ahead in few_up spills and
+// costs 2 us; Up brought into L2 during the product gains nothing.
 //
 // A dot product does not care in which order K is taken: lane t of a fragment's four reads
 // eight consecutive values, in both operands alike, where the fragment's layout would give

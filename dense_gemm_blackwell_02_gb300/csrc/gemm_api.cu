@@ -707,9 +707,13 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
   const int out = out_kind(dtype_out);
   const bool fp8_in = is_fp8(dtype_in);
   // A few rows of A: the CUDA-core matrix-vector path (variant 3), forced or automatic.
+  // (Beside adapters a large matrix is faster in tiles, whose CTAs leave room for the other
+  // kernel: one adapter of rank 16, N x K, us: 8192 x 8192 31.6 against 33.2, 14336 x 4096
+  // 26.5 and 28.4, 14336 x 14336 71.7 and 78.5; 8192 x 2048 14.1 and 13.1.)
   const gemm_config_t& fc = h->forced;
+  const bool tiles_beside = h->beside_rows && N >= 8192 && K >= 4096;
   if (fc.variant == 3 || (!fc.variant && !fc.block_n && !fc.splits && !fc.stages && !fc.epilogue &&
-                          !fc.chain_kblocks && fc.swap_ab != 2 && M == 1 && K <= kGemvAutoMaxK &&
+                          !fc.chain_kblocks && fc.swap_ab != 2 && M == 1 && K <= kGemvAutoMaxK && !tiles_beside &&
                           !fused && !fp8_in && !bs && !ad)) {
     if (M > kGemvMaxRows || fused || fp8_in || bs || ad) return GEMM_ERR_UNSUPPORTED;
     GemvSpec g;
