@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 F16, BF16, F32, E4M3, E5M2 = 0, 1, 2, 3, 4
 STATUS_NAMES = {0: "GEMM_OK", 1: "GEMM_ERR_INVALID_ARG", 2: "GEMM_ERR_UNSUPPORTED",
@@ -16,7 +17,8 @@ STATUS_NAMES = {0: "GEMM_OK", 1: "GEMM_ERR_INVALID_ARG", 2: "GEMM_ERR_UNSUPPORTE
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm.so")
 
 # Every function include/gemm.h declares (checked against the header by the tests).
-EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_epilogue", "gemm_run_blockwise",
+EXPORTS = ("gemm_run_adapters_packed", "gemm_rotary_packed", "gemm_adjust_logits_packed",
+           "gemm_create", "gemm_destroy", "gemm_run", "gemm_run_epilogue", "gemm_run_blockwise",
            "gemm_run_grouped", "gemm_run_host",
            "gemm_set_config",
            "gemm_last_config", "gemm_device_status", "gemm_set_wait_limit",
@@ -153,6 +155,8 @@ def lib():
     L.gemm_rotary.argtypes = [vp, vp, vp] + [i64] * 7 + [i32, ctypes.POINTER(GemmRotary), vp]
     L.gemm_adjust_logits.argtypes = [vp, vp, vp] + [i64] * 4 + [i32, i32,
                                                                 ctypes.POINTER(GemmLogits), vp]
+    for name in ("gemm_run_adapters_packed", "gemm_rotary_packed", "gemm_adjust_logits_packed"):
+        getattr(L, name).argtypes = [ctypes.c_char_p]
     L.gemm_status_string.argtypes = [i32]
     L.gemm_status_string.restype = ctypes.c_char_p
     L.gemm_plan.argtypes = [ctypes.POINTER(GemmDeviceModel), ctypes.POINTER(GemmConfig), i64, i64,
@@ -199,15 +203,32 @@ def torch_dtype_code(dt) -> int:
 
 
 def _need(t, name, dtype, shape, index):
-    """Check an auxiliary tensor (None stays None) on CUDA device `index` and give its
-    address."""
+    """Check an auxiliary tensor on CUDA device `index` and give its address (0 for None)."""
     if t is None:
-        return None
+        return 0
     if (t.get_device() != index or t.dtype is not dtype or not t.is_contiguous()
             or (shape is not None and t.shape != shape)):
         want = "" if shape is None else f" of shape {tuple(shape)}"
         raise ValueError(f"{name} must be a contiguous {dtype} tensor{want} on cuda:{index}")
     return t.data_ptr()
+
+
+def _vec(t, name, dtype, n, index):
+    """_need for a vector of n values; 0 for None."""
+    if t is None:
+        return 0
+    if (t.dtype is not dtype or t.dim() != 1 or t.size(0) != n or t.get_device() != index
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},) on cuda:{index}")
+    return t.data_ptr()
+
+
+# The blocks of the packed calls (gemm_adapters_call_t, gemm_rotary_call_t,
+# gemm_logits_call_t).  A block costs a microsecond; a dozen arguments through ctypes and a
+# structure, three.
+_ADAPTERS_CALL = struct.Struct("PPPPqqqPPiiPPPii")
+_ROTARY_CALL = struct.Struct("PPPqqqqqqqP" "PPPPqiiii" "ii")
+_LOGITS_CALL = struct.Struct("PPPqqqqPii" "PPPPPPPPPPqqP")
 
 
 def pair_axes(sections, interleaved=False):
@@ -382,18 +403,16 @@ class Gemm:
         if X.dim() != 2 or W.dim() != 2 or down.dim() != 3:
             raise ValueError("X and W must be 2-D, down and up 3-D")
         M, K = X.shape
-        N = W.shape[0]
+        N = W.size(0)
         count, rank, _ = down.shape
-        dev, dt = X.get_device(), X.dtype
-        ad = GemmAdapters(_need(down, "down", dt, (count, rank, K), dev),
-                          _need(up, "up", dt, (count, N, rank), dev),
-                          _need(scale, "scale", _torch.float32, (count,), dev), count, rank)
-        code = _lib.gemm_run_adapters(self._h, _need(X, "X", dt, (M, K), dev),
-                                      _need(W, "W", dt, (N, K), dev),
-                                      _need(Y, "Y", Y.dtype, (M, N), dev), M, N, K,
-                                      _DTYPE_CODE[dt], _DTYPE_CODE[Y.dtype], ctypes.byref(ad),
-                                      _need(row_adapter, "row_adapter", _torch.int32, (M,), dev),
-                                      _stream_of(stream, dev))
+        dev, dt, out = X.get_device(), X.dtype, Y.dtype
+        code = _lib.gemm_run_adapters_packed(_ADAPTERS_CALL.pack(
+            self._h.value or 0, _need(X, "X", dt, None, dev), _need(W, "W", dt, (N, K), dev),
+            _need(Y, "Y", out, (M, N), dev), M, N, K,
+            _vec(row_adapter, "row_adapter", _torch.int32, M, dev), _stream_of(stream, dev),
+            _DTYPE_CODE[dt], _DTYPE_CODE[out], _need(down, "down", dt, (count, rank, K), dev),
+            _need(up, "up", dt, (count, N, rank), dev),
+            _vec(scale, "scale", _torch.float32, count, dev), count, rank))
         if code:
             _check(code, f"gemm_run_adapters M={M} N={N} K={K} rank={rank}", self._h)
         return Y
@@ -421,20 +440,22 @@ class Gemm:
             raise ValueError("cos and sin must be (positions, pairs), positions (axes, tokens)")
         P, half = cos.shape
         axes = positions.shape[0]
+        follow = b""
         if pair_axis is not None:
             if len(pair_axis) != half:
                 raise ValueError(f"pair_axis must name an axis for each of the {half} pairs")
-            pair_axis = bytes(pair_axis)
-            if half and max(pair_axis) >= axes:
-                raise ValueError(f"pair_axis must hold axes below {axes}")
+            follow = bytes(pair_axis)
         f32 = _torch.float32
-        r = GemmRotary(_need(cos, "cos", f32, (P, half), dev), _need(sin, "sin", f32, (P, half), dev),
-                       _need(positions, "positions", _torch.int32, (axes, T), dev), pair_axis, P,
-                       axes, 2 * half, PAIRS_NEIGHBOURS if neighbours else PAIRS_HALF,
-                       1 if inverse else 0)
-        code = _lib.gemm_rotary(self._h, x.data_ptr(), y.data_ptr(), T, H, D, xt, xh, yt, yh,
-                                _DTYPE_CODE[dt], ctypes.byref(r), _stream_of(stream, dev))
+        code = _lib.gemm_rotary_packed(_ROTARY_CALL.pack(
+            self._h.value or 0, x.data_ptr(), y.data_ptr(), T, H, D, xt, xh, yt, yh,
+            _stream_of(stream, dev), _need(cos, "cos", f32, None, dev),
+            _need(sin, "sin", f32, (P, half), dev),
+            _need(positions, "positions", _torch.int32, (axes, T), dev), 0, P, axes, 2 * half,
+            PAIRS_NEIGHBOURS if neighbours else PAIRS_HALF, 1 if inverse else 0, _DTYPE_CODE[dt],
+            1 if follow else 0) + follow)
         if code:
+            if follow and max(follow) >= axes:
+                raise ValueError(f"pair_axis must hold axes below {axes}")
             _check(code, f"gemm_rotary tokens={T} heads={H} dim={D}", self._h)
         return y
 
@@ -468,21 +489,21 @@ class Gemm:
             if mask.dim() != 2:
                 raise ValueError("mask must be (masks, words)")
             masks, words = mask.shape
-        a = GemmLogits(_need(tokens, "tokens", i32, None, dev),
-                       _need(token_start, "token_start", i64, (B + 1,), dev),
-                       _need(prompt_len, "prompt_len", i32, (B,), dev),
-                       _need(repetition, "repetition", f32, (B,), dev),
-                       _need(frequency, "frequency", f32, (B,), dev),
-                       _need(presence, "presence", f32, (B,), dev),
-                       _need(bias_tokens, "bias_tokens", i32, None, dev),
-                       _need(bias_values, "bias_values", f32,
-                             None if bias_tokens is None else bias_tokens.shape, dev),
-                       _need(bias_start, "bias_start", i64, (B + 1,), dev),
-                       _need(mask, "mask", i32, None, dev), words, masks,
-                       _need(mask_row, "mask_row", i32, (B,), dev))
-        code = _lib.gemm_adjust_logits(self._h, logits.data_ptr(), out.data_ptr(), B, V, sl, so,
-                                       _DTYPE_CODE[logits.dtype], _DTYPE_CODE[out.dtype],
-                                       ctypes.byref(a), _stream_of(stream, dev))
+        code = _lib.gemm_adjust_logits_packed(_LOGITS_CALL.pack(
+            self._h.value or 0, logits.data_ptr(), out.data_ptr(), B, V, sl, so,
+            _stream_of(stream, dev), _DTYPE_CODE[logits.dtype], _DTYPE_CODE[out.dtype],
+            _need(tokens, "tokens", i32, None, dev),
+            _vec(token_start, "token_start", i64, B + 1, dev),
+            _vec(prompt_len, "prompt_len", i32, B, dev),
+            _vec(repetition, "repetition", f32, B, dev),
+            _vec(frequency, "frequency", f32, B, dev),
+            _vec(presence, "presence", f32, B, dev),
+            _need(bias_tokens, "bias_tokens", i32, None, dev),
+            _need(bias_values, "bias_values", f32,
+                  None if bias_tokens is None else bias_tokens.shape, dev),
+            _vec(bias_start, "bias_start", i64, B + 1, dev),
+            _need(mask, "mask", i32, None, dev), words, masks,
+            _vec(mask_row, "mask_row", i32, B, dev)))
         if code:
             _check(code, f"gemm_adjust_logits rows={B} vocab={V}", self._h)
         return out

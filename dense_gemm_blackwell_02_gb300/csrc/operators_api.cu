@@ -325,4 +325,28 @@ gemm_status_t gemm_adjust_logits(gemm_handle_t h, const void* logits, void* out,
   return launched(h, launch_logits(p, dtype_in, dtype_out, h->sms, reinterpret_cast<cudaStream_t>(stream_)));
 }
 
+gemm_status_t gemm_run_adapters_packed(const gemm_adapters_call_t* c) {
+  if (!c) return GEMM_ERR_INVALID_ARG;
+  return gemm_run_adapters(c->h, c->X, c->W, c->Y, c->M, c->N, c->K,
+                           static_cast<gemm_dtype_t>(c->dtype_in),
+                           static_cast<gemm_dtype_t>(c->dtype_out), &c->adapters, c->row_adapter,
+                           c->stream);
+}
+
+gemm_status_t gemm_rotary_packed(const gemm_rotary_call_t* c) {
+  if (!c) return GEMM_ERR_INVALID_ARG;
+  gemm_rotary_t r = c->rotary;
+  if (c->axes_follow) r.pair_axis = reinterpret_cast<const uint8_t*>(c + 1);
+  return gemm_rotary(c->h, c->x, c->y, c->tokens, c->heads, c->dim, c->x_token_stride,
+                     c->x_head_stride, c->y_token_stride, c->y_head_stride,
+                     static_cast<gemm_dtype_t>(c->dtype), &r, c->stream);
+}
+
+gemm_status_t gemm_adjust_logits_packed(const gemm_logits_call_t* c) {
+  if (!c) return GEMM_ERR_INVALID_ARG;
+  return gemm_adjust_logits(c->h, c->logits, c->out, c->rows, c->vocab, c->logits_stride,
+                            c->out_stride, static_cast<gemm_dtype_t>(c->dtype_in),
+                            static_cast<gemm_dtype_t>(c->dtype_out), &c->adjust, c->stream);
+}
+
 }  // extern "C"

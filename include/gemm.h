@@ -567,6 +567,50 @@ gemm_status_t gemm_adjust_logits(gemm_handle_t h, const void* logits, void* out,
                                  gemm_dtype_t dtype_in, gemm_dtype_t dtype_out,
                                  const gemm_logits_t* adjust, gemm_stream_t stream);
 
+/*
+ * gemm_run_adapters, gemm_rotary and gemm_adjust_logits with their arguments in one block
+ * of host memory, for a foreign-function interface that takes its time for every argument.
+ * The fields are the calls' arguments; the results and errors are theirs, and a NULL block
+ * gives GEMM_ERR_INVALID_ARG.
+ */
+typedef struct {
+  gemm_handle_t h;
+  const void* X;
+  const void* W;
+  void* Y;
+  int64_t M, N, K;
+  const int32_t* row_adapter;
+  gemm_stream_t stream;
+  int32_t dtype_in, dtype_out; /* gemm_dtype_t */
+  gemm_adapters_t adapters;
+} gemm_adapters_call_t;
+
+typedef struct {
+  gemm_handle_t h;
+  const void* x;
+  void* y;
+  int64_t tokens, heads, dim;
+  int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+  gemm_stream_t stream;
+  gemm_rotary_t rotary;
+  int32_t dtype;       /* gemm_dtype_t */
+  int32_t axes_follow; /* nonzero: pair_axis is the rot_dim / 2 bytes after this block */
+} gemm_rotary_call_t;
+
+typedef struct {
+  gemm_handle_t h;
+  const void* logits;
+  void* out;
+  int64_t rows, vocab, logits_stride, out_stride;
+  gemm_stream_t stream;
+  int32_t dtype_in, dtype_out; /* gemm_dtype_t */
+  gemm_logits_t adjust;
+} gemm_logits_call_t;
+
+gemm_status_t gemm_run_adapters_packed(const gemm_adapters_call_t* call);
+gemm_status_t gemm_rotary_packed(const gemm_rotary_call_t* call);
+gemm_status_t gemm_adjust_logits_packed(const gemm_logits_call_t* call);
+
 #ifdef __cplusplus
 }
 #endif
