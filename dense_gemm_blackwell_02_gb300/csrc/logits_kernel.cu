@@ -18,7 +18,8 @@
 // size, the same; copying first and then rewriting only the logits that the lists name, 70 us
 // (each of the row's slices goes through the history twice); the same from a list of the
 // distinct tokens, 65; the row's CTAs as a cluster that counts in distributed shared memory,
-// 92 (remote atomics).
+// 92 (remote atomics); a warp's listed logits gathered in shared memory at every step and
+// adjusted side by side, 84 (its registers spill at three CTAs per SM).
 #include <algorithm>
 
 #include "elements.cuh"
