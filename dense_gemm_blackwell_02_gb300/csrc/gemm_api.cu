@@ -440,9 +440,8 @@ gemm_status_t choose_plain(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out
 //
 // A grid that takes more than the product's share of the SMs, by the rows that either kernel
 // streams: the largest grid within that share, else the smallest that is a quarter of the
-// SMs.  The other kernel has room for one CTA next
-// to one of the product's, for six on an SM of its own, and both are bound by how much they
-// keep in flight (with 64 adapters of rank 64, 256 x 8192 x 8192: 64 CTAs 65 us against 88
+// SMs.  The other kernel has room for one CTA next to one of the product's, for six on an SM
+// of its own, and both are bound by how much they keep in flight (with 64 adapters of rank 64, 256 x 8192 x 8192: 64 CTAs 65 us against 88
 // for 128; 256 x 4096 x 4096 30 against 45; with 16 of rank 64, 256 x 8192 x 8192: 104 CTAs
 // 48 against 58; with 64 of rank 16, 256 x 10240 x 8192: 128 CTAs 54 against 62 for
 // stream-K on 152).
@@ -460,7 +459,8 @@ void choose_beside(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int kb
   const int64_t narrow = ceil_div(M, (int64_t)kBlockM) * ceil_div(N, (int64_t)128);
   if (!c->kx2 && !c->sk_workers && c->dp_tiles == 0 && c->splits >= 3) {
     const int64_t s = std::min<int64_t>({h->sms / narrow, c->k_blocks / 16, 8});
-    forced(1, 128, (int)std::max<int64_t>(1, s), 0, c);
+    Choice to;
+    if (forced(1, 128, (int)std::max<int64_t>(1, s), 0, &to)) *c = to;
   }
   const int64_t share = h->sms * N / (N + h->beside_rows);
   if (c->grid <= share) return;

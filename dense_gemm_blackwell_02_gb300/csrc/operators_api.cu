@@ -53,9 +53,10 @@ gemm_status_t ensure_scratch(gemm_ctx* h, size_t bytes, size_t counters) {
 }
 
 // What the shared product of a call takes in place of gemm_run's choices.  Binary32 results:
-// accumulation chains of K 256.  The tensor cores' error grows with a chain's length; at the default K 4096 it was 1.2e-6 of the result
-// (relative Frobenius), where sums in binary32 have 2.4e-7.  16-bit results round by 1000
-// times that.
+// accumulation chains of K 256.  The tensor cores' error grows with a chain's length; at the
+// default K 4096 it was 1.2e-6 of the result (relative Frobenius), where sums in binary32 have
+// 2.4e-7.  16-bit results round by 1000 times that.  For few rows, the rows of Down that are
+// streamed beside the product and the pitch of its result.
 constexpr int kShortChain = 4;  // K blocks
 struct ProductRules {
   gemm_ctx* h;
