@@ -217,7 +217,7 @@ def _vec(t, name, dtype, n, index):
     """_need for a vector of n values; 0 for None."""
     if t is None:
         return 0
-    if (t.dtype is not dtype or t.dim() != 1 or t.size(0) != n or t.get_device() != index
+    if (t.dtype is not dtype or t.shape != (n,) or t.get_device() != index
             or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},) on cuda:{index}")
     return t.data_ptr()
@@ -403,7 +403,7 @@ class Gemm:
         if X.dim() != 2 or W.dim() != 2 or down.dim() != 3:
             raise ValueError("X and W must be 2-D, down and up 3-D")
         M, K = X.shape
-        N = W.size(0)
+        N = W.shape[0]
         count, rank, _ = down.shape
         dev, dt, out = X.get_device(), X.dtype, Y.dtype
         code = _lib.gemm_run_adapters_packed(_ADAPTERS_CALL.pack(

@@ -35,6 +35,7 @@ constexpr int kOcc = 3;            // CTAs per SM
 constexpr int kVec = 8;            // logits per thread and step
 constexpr int kTokens = 8;         // history tokens per thread in flight
 constexpr int kMaxSlice = 24576;   // tokens per CTA: 48 KiB of table
+static_assert(kMaxSlice * 2 <= 48 * 1024, "more would have to be asked for at every launch");
 constexpr int kMinSlice = 2048;
 
 // A token's entry in the table: how often it was generated, and two flags; 16 bits or 32.
@@ -230,11 +231,6 @@ template <typename TI, typename TO, bool TABLE>
 cudaError_t launch(const LogitsParams& p, cudaStream_t stream) {
   const size_t smem = TABLE ? (size_t)p.slice * 2 : 0;
   auto kernel = logits_kernel<TI, TO, TABLE>;
-  if (TABLE) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxSlice * 2);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)p.rows * p.slices), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
