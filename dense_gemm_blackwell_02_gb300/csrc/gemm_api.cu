@@ -15,6 +15,7 @@
 #include "context.h"
 #include "gemm.h"
 #include "launch.h"
+#include "scratch.h"
 #include "umma.cuh"
 
 using namespace gb300;
@@ -540,8 +541,9 @@ gemm_status_t ensure_workspace(gemm_ctx* h, size_t ws_bytes, size_t ctr_count) {
     if (h->d_ctr) cudaFree(h->d_ctr);
     h->d_ctr = nullptr;
     h->ctr_count = 0;
-    if (cudaMalloc(&h->d_ctr, ctr_count * sizeof(uint32_t)) != cudaSuccess) return GEMM_ERR_OOM;
-    if (cudaMemset(h->d_ctr, 0, ctr_count * sizeof(uint32_t)) != cudaSuccess) return GEMM_ERR_CUDA;
+    const gemm_status_t st =
+        make_cleared(reinterpret_cast<void**>(&h->d_ctr), ctr_count * sizeof(uint32_t));
+    if (st != GEMM_OK) return st;
     h->ctr_count = ctr_count;
   }
   return GEMM_OK;
@@ -583,14 +585,10 @@ gemm_status_t gemm_create(gemm_handle_t* out) {
   if (!h) return GEMM_ERR_OOM;
   h->device = dev;
   h->sms = sms;
-  if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess) {
+  const gemm_status_t st = make_cleared(reinterpret_cast<void**>(&h->d_status), sizeof(uint32_t));
+  if (st != GEMM_OK) {
     delete h;
-    return GEMM_ERR_OOM;
-  }
-  if (cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
-    cudaFree(h->d_status);
-    delete h;
-    return GEMM_ERR_CUDA;
+    return st;
   }
   *out = h;
   return GEMM_OK;

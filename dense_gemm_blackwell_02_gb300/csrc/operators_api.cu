@@ -11,6 +11,7 @@
 #include "context.h"
 #include "gemm.h"
 #include "operators.h"
+#include "scratch.h"
 #include "umma.cuh"
 
 using namespace gb300;
@@ -42,11 +43,9 @@ gemm_status_t ensure_scratch(gemm_ctx* h, size_t bytes, size_t counters) {
     if (h->d_op_ctr) cudaFree(h->d_op_ctr);
     h->d_op_ctr = nullptr;
     h->op_ctr_count = 0;
-    if (cudaMalloc(&h->d_op_ctr, counters * sizeof(uint32_t)) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_OOM;
-    }
-    if (cudaMemset(h->d_op_ctr, 0, counters * sizeof(uint32_t)) != cudaSuccess) return GEMM_ERR_CUDA;
+    const gemm_status_t st =
+        make_cleared(reinterpret_cast<void**>(&h->d_op_ctr), counters * sizeof(uint32_t));
+    if (st != GEMM_OK) return st;
     h->op_ctr_count = counters;
   }
   return GEMM_OK;
