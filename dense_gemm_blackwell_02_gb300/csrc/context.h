@@ -10,6 +10,7 @@
 
 #include "gemm.h"
 #include "params.h"
+#include "scratch.h"
 
 namespace gb300 {
 
@@ -38,16 +39,12 @@ struct gemm_ctx {
   cudaError_t last_cuda = cudaSuccess;  // the CUDA error behind the last GEMM_ERR_CUDA launch
   int sms = 0;
   uint32_t* d_status = nullptr;
-  float* d_ws = nullptr;
-  size_t ws_bytes = 0;
-  uint32_t* d_ctr = nullptr;
-  size_t ctr_count = 0;
+  gb300::Scratch ws;        // partial tiles of a product cut along K
+  gb300::Scratch ctr;       // its arrival counters, zero between calls
   void* d_stage[3] = {nullptr, nullptr, nullptr};  // gemm_run_host: A, B, C
   size_t stage_bytes[3] = {0, 0, 0};
-  void* d_op = nullptr;  // scratch of the operators around the projections
-  size_t op_bytes = 0;
-  uint32_t* d_op_ctr = nullptr;
-  size_t op_ctr_count = 0;
+  gb300::Scratch op;        // scratch of the operators around the projections
+  gb300::Scratch op_ctr;    // their counters, zero between calls
   gemm_config_t forced = {};
   int32_t short_chains = 0;  // K blocks per accumulation chain where none is forced (0: the default)
   // elements per row of C where not N: a whole number of 16 bytes; C is then written by TMA

@@ -15,7 +15,6 @@
 #include "context.h"
 #include "gemm.h"
 #include "launch.h"
-#include "scratch.h"
 #include "umma.cuh"
 
 using namespace gb300;
@@ -530,23 +529,8 @@ gemm_status_t choose(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int 
 }
 
 gemm_status_t ensure_workspace(gemm_ctx* h, size_t ws_bytes, size_t ctr_count) {
-  if (ws_bytes > h->ws_bytes) {
-    if (h->d_ws) cudaFree(h->d_ws);
-    h->d_ws = nullptr;
-    h->ws_bytes = 0;
-    if (cudaMalloc(&h->d_ws, ws_bytes) != cudaSuccess) return GEMM_ERR_OOM;
-    h->ws_bytes = ws_bytes;
-  }
-  if (ctr_count > h->ctr_count) {
-    if (h->d_ctr) cudaFree(h->d_ctr);
-    h->d_ctr = nullptr;
-    h->ctr_count = 0;
-    const gemm_status_t st =
-        make_cleared(reinterpret_cast<void**>(&h->d_ctr), ctr_count * sizeof(uint32_t));
-    if (st != GEMM_OK) return st;
-    h->ctr_count = ctr_count;
-  }
-  return GEMM_OK;
+  const gemm_status_t st = h->ws.grow(ws_bytes, false);
+  return st != GEMM_OK ? st : h->ctr.grow(ctr_count * sizeof(uint32_t), true);
 }
 
 }  // namespace
@@ -598,10 +582,7 @@ gemm_status_t gemm_destroy(gemm_handle_t h) {
   if (!h) return GEMM_OK;
   cudaDeviceSynchronize();
   cudaFree(h->d_status);
-  if (h->d_ws) cudaFree(h->d_ws);
-  if (h->d_ctr) cudaFree(h->d_ctr);
-  if (h->d_op) cudaFree(h->d_op);
-  if (h->d_op_ctr) cudaFree(h->d_op_ctr);
+  for (Scratch* s : {&h->ws, &h->ctr, &h->op, &h->op_ctr}) s->release();
   for (auto* p : h->d_stage)
     if (p) cudaFree(p);
   if (h->copy_in) cudaStreamDestroy(h->copy_in);
@@ -867,8 +848,8 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
     const size_t ws = sliced * ch.ws_slots * kBlockM * ch.variant * ch.bn * sizeof(float);
     st = ensure_workspace(h, ws, sliced * ch.variant * 8);
     if (st != GEMM_OK) return st;
-    p.workspace = h->d_ws;
-    p.counters = h->d_ctr;
+    p.workspace = static_cast<float*>(h->ws.ptr);
+    p.counters = static_cast<uint32_t*>(h->ctr.ptr);
   }
   if (before && (h->last_cuda = (*before)()) != cudaSuccess) return GEMM_ERR_CUDA;
   if ((h->last_cuda = launch_gemm(s)) != cudaSuccess) return GEMM_ERR_CUDA;
@@ -1139,10 +1120,10 @@ gemm_status_t gemm_device_status(gemm_handle_t h, gemm_stream_t stream_, uint32_
     return GEMM_ERR_CUDA;
   if (detail) *detail = word;
   if (word == 0) return GEMM_OK;
-  // An aborted split-K run (or slices of adapters) may leave arrival counters behind: clear them too.
+  // An aborted run may leave the counters of K slices behind: clear them, and those of the
+  // adapters' groups, too.
   cudaMemset(h->d_status, 0, sizeof(uint32_t));
-  if (h->d_ctr) cudaMemset(h->d_ctr, 0, h->ctr_count * sizeof(uint32_t));
-  if (h->d_op_ctr) cudaMemset(h->d_op_ctr, 0, h->op_ctr_count * sizeof(uint32_t));
+  for (Scratch* s : {&h->ctr, &h->op_ctr}) s->clear();
   if (cudaDeviceSynchronize() != cudaSuccess) return GEMM_ERR_CUDA;
   return (word >> 24) == kDevBadIndex ? GEMM_ERR_BAD_INDEX : GEMM_ERR_TIMEOUT;
 }

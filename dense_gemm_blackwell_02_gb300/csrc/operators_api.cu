@@ -11,7 +11,6 @@
 #include "context.h"
 #include "gemm.h"
 #include "operators.h"
-#include "scratch.h"
 #include "umma.cuh"
 
 using namespace gb300;
@@ -29,26 +28,8 @@ size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
 // The handle's scratch for these operators, grown on demand; its counters are zero between
 // calls.
 gemm_status_t ensure_scratch(gemm_ctx* h, size_t bytes, size_t counters) {
-  if (bytes > h->op_bytes) {
-    if (h->d_op) cudaFree(h->d_op);
-    h->d_op = nullptr;
-    h->op_bytes = 0;
-    if (cudaMalloc(&h->d_op, bytes) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_OOM;
-    }
-    h->op_bytes = bytes;
-  }
-  if (counters > h->op_ctr_count) {
-    if (h->d_op_ctr) cudaFree(h->d_op_ctr);
-    h->d_op_ctr = nullptr;
-    h->op_ctr_count = 0;
-    const gemm_status_t st =
-        make_cleared(reinterpret_cast<void**>(&h->d_op_ctr), counters * sizeof(uint32_t));
-    if (st != GEMM_OK) return st;
-    h->op_ctr_count = counters;
-  }
-  return GEMM_OK;
+  const gemm_status_t st = h->op.grow(bytes, false);
+  return st != GEMM_OK ? st : h->op_ctr.grow(counters * sizeof(uint32_t), true);
 }
 
 // What the shared product of a call takes in place of gemm_run's choices.  Binary32 results:
@@ -140,7 +121,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     gemm_status_t st = ensure_scratch(
         h, base_bytes + part_bytes + (size_t)M * sizeof(FewGroup), 2);
     if (st != GEMM_OK) return st;
-    char* scratch = static_cast<char*>(h->d_op);
+    char* scratch = static_cast<char*>(h->op.ptr);
     void* base = base_in_y ? Y : scratch;
     h->beside_rows = few_down_rows((int32_t)M, ad->rank, ad->count);
     if (f.base_pitch != N) h->c_pitch = f.base_pitch;
@@ -160,7 +141,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     f.vec_base = aligned(base, 16) && f.base_pitch % 4 == 0;
     f.partial = reinterpret_cast<float*>(scratch + base_bytes);
     f.groups = reinterpret_cast<FewGroup*>(scratch + base_bytes + part_bytes);
-    f.counts = h->d_op_ctr;
+    f.counts = static_cast<uint32_t*>(h->op_ctr.ptr);
     f.base = static_cast<const float*>(base);
     f.Y = Y;
     f.status = h->d_status;
@@ -196,7 +177,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   const size_t scale_bytes = round_up((size_t)M * sizeof(float));
   gemm_status_t st = ensure_scratch(h, u_bytes + scale_bytes + (size_t)pairs * sizeof(AdapterTile), 0);
   if (st != GEMM_OK) return st;
-  char* scratch = static_cast<char*>(h->d_op);
+  char* scratch = static_cast<char*>(h->op.ptr);
   p.U = scratch;
   p.row_scale = reinterpret_cast<float*>(scratch + u_bytes);
   p.pairs = reinterpret_cast<AdapterTile*>(scratch + u_bytes + scale_bytes);

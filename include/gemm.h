@@ -20,7 +20,8 @@
  * owns its split-K workspace, its device status word, its tensor-map cache and
  * the staging buffers of gemm_run_host.  One handle serves one host thread and
  * one stream at a time: calls that overlap on the GPU through one handle race
- * on its workspace.
+ * on its workspace.  A workspace that a later call outgrows is kept until
+ * gemm_destroy, so that a graph captured through the handle can be replayed.
  *
  * Errors.  Every call returns a gemm_status_t.  Argument problems are reported
  * synchronously and nothing is launched.  gemm_run is asynchronous: a kernel

@@ -57,3 +57,36 @@ def test_first_call_on_a_side_stream_while_the_default_one_is_busy(M):
             g.run_adapters(X, W, Y, down, up, ids, stream=side)
             side.synchronize()
             assert _near(Y, want)
+
+
+def test_a_captured_graph_replays_after_larger_calls_of_its_handle():
+    from dense_gemm_blackwell_02_gb300.binding import Gemm
+    small, large = _adapted(64), _adapted(8192, N=1040)
+    Y, Z = (torch.empty(t[5].shape, device="cuda") for t in (small, large))
+    A, B = small[0].new_ones(256, 16384), small[0].new_ones(200, 16384)
+    C, D = torch.empty(256, 200, device="cuda"), torch.empty(1024, 1000, device="cuda")
+    with Gemm() as g:
+        def step():
+            g.run_adapters(*small[:2], Y, *small[2:5])
+            g.run(A, B, C)                     # cut along K: workspace and counters
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        g.run_adapters(*large[:2], Z, *large[2:5])
+        g.run(A.new_ones(1024, 16384), A.new_ones(1000, 16384), D)
+        other = torch.full((1 << 26,), float("nan"), device="cuda")   # what freed memory would hold
+        torch.cuda.synchronize()
+        for _ in range(3):
+            Y.fill_(float("nan"))
+            C.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert _near(Y, small[5]) and (C == 16384).all()
+        assert _near(Z, large[5]) and (D == 16384).all()
+        assert torch.isnan(other).all()
+        assert g.device_status() == (0, 0)
