@@ -224,18 +224,18 @@ __host__ __device__ constexpr int up_ctas_per_sm(int rc) { return rc <= 16 ? 6 :
 
 // Grid: x a share of Y's columns, y the group.  RC: the rank's class, 16, 32, 64 or 128.  A
 // warp takes 32 columns at a time, and loads the next ones' weights and base before it
-// multiplies the present ones'.  u enters the MMA as two 16-bit parts, u = 2^e (hi + lo), e
-// the exponent of the row's largest value in fp16 (whose range would cut u off) and 0 in
-// bf16; at least 17 bits of u reach the product.
+// multiplies the present ones'.  u enters the MMA as 16-bit parts, u = 2^e (first + second
+// ...), e the exponent of the row's largest value in fp16 (whose range would cut u off) and 0
+// in bf16.
 template <typename T, typename TO, int RC>
 __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
     few_up_kernel(const __grid_constant__ AdapterFewParams p) {
   using C = typename Chunk<RC>::type;
   constexpr int kValues = Chunk<RC>::kValues;       // of a row per lane and chunk
   constexpr int kChunks = RC / (4 * kValues);       // chunks of a row
-  constexpr int kPitch = RC + 8;  // values per row of hi and lo: rows on different banks
-  __shared__ alignas(16) T hi[kRows * kPitch];
-  __shared__ alignas(16) T lo[kRows * kPitch];
+  constexpr int kPitch = RC + 8;  // values per row of a part: rows on different banks
+  constexpr int P = u_parts(std::is_same<T, __nv_bfloat16>::value, std::is_same<TO, float>::value);
+  __shared__ alignas(16) T part[P][kRows * kPitch];
   __shared__ float row_scale[kRows];
   __shared__ float turn[kWarps][8][33];
   const int tid = (int)threadIdx.x, warp = (int)warp_id(), lane = (int)lane_id();
@@ -354,15 +354,16 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
         }
         if (i < kRows) {
           if (c == 0) row_scale[i] = back;
-          Pack<T, 8> h, l;
+          Pack<T, 8> to[P];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float x = v[k] * inv;
-            h.v[k] = from_f32<T>(x);
-            l.v[k] = from_f32<T>(isinf(to_f32(h.v[k])) ? 0.0f : x - to_f32(h.v[k]));
+            T x[P];
+            split_f32(v[k] * inv, x);
+#pragma unroll
+            for (int j = 0; j < P; ++j) to[j].v[k] = x[j];
           }
-          *reinterpret_cast<Pack<T, 8>*>(hi + i * kPitch + c) = h;
-          *reinterpret_cast<Pack<T, 8>*>(lo + i * kPitch + c) = l;
+#pragma unroll
+          for (int j = 0; j < P; ++j) *reinterpret_cast<Pack<T, 8>*>(part[j] + i * kPitch + c) = to[j];
         }
       }
       __syncthreads();
@@ -384,15 +385,16 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           const int k = (4 * c + t) * kValues;
-          const C h0 = *reinterpret_cast<const C*>(hi + g * kPitch + k);
-          const C h1 = *reinterpret_cast<const C*>(hi + (g + 8) * kPitch + k);
-          const C l0 = *reinterpret_cast<const C*>(lo + g * kPitch + k);
-          const C l1 = *reinterpret_cast<const C*>(lo + (g + 8) * kPitch + k);
+          C u0[P], u1[P];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mma_chunk<T>(acc[j], h0, h1, b[c][j]);
-            mma_chunk<T>(acc[j], l0, l1, b[c][j]);
+          for (int s = 0; s < P; ++s) {
+            u0[s] = *reinterpret_cast<const C*>(part[s] + g * kPitch + k);
+            u1[s] = *reinterpret_cast<const C*>(part[s] + (g + 8) * kPitch + k);
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = 0; s < P; ++s) mma_chunk<T>(acc[j], u0[s], u1[s], b[c][j]);
         }
       }
 #pragma unroll

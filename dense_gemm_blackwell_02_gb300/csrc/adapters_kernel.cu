@@ -19,9 +19,9 @@
 // u take the rest: the latency of its steps bounds it, not X's 17 MB.  Asking for X ahead of
 // the rows' adapters (into L2) delays the first K block by 2 us.
 //
-// u leaves as two 16-bit parts, u = 2^e (hi + lo) with e the exponent of the row's largest
-// value: fp16's range cannot cut it off, and at least 17 of its bits reach the second product
-// (one part alone would round u to 8 or 11 bits, an error of the size of Y's own rounding).
+// u leaves as 16-bit parts, u = 2^e (first + second ...) with e the exponent of the row's
+// largest value, which brings them into fp16's range: one part alone would round u to 8 or 11
+// bits, an error of the size of Y's own rounding (how many, and what they leave: u_parts).
 #include <algorithm>
 
 #include "elements.cuh"
@@ -168,18 +168,19 @@ __device__ __forceinline__ void row_factors(float big, float& inv, float& back) 
   back = __uint_as_float((uint32_t)e << 23);
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void store_parts(T* hi, T* lo, const float (&v)[N], float inv) {
-  struct alignas(N * sizeof(T)) { T x[N]; } h, l;
+// N values times inv as P parts, kBlockK values apart.
+template <typename T, int N, int P>
+__device__ __forceinline__ void store_parts(T* to, const float (&v)[N], float inv) {
+  struct alignas(N * sizeof(T)) { T x[N]; } part[P];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const float x = v[k] * inv;
-    h.x[k] = from_f32<T>(x);
-    const float f = to_f32(h.x[k]);
-    l.x[k] = from_f32<T>(isinf(f) ? 0.0f : x - f);
+    T x[P];
+    split_f32(v[k] * inv, x);
+#pragma unroll
+    for (int j = 0; j < P; ++j) part[j].x[k] = x[j];
   }
-  *reinterpret_cast<decltype(h)*>(hi) = h;
-  *reinterpret_cast<decltype(l)*>(lo) = l;
+#pragma unroll
+  for (int j = 0; j < P; ++j) *reinterpret_cast<decltype(&part[0])>(to + j * kBlockK) = part[j];
 }
 
 // The adapters of two row tiles, as the GEMM's 256-row tile takes them.
@@ -239,7 +240,8 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-template <typename T>
+// P: the parts of u.
+template <typename T, int P>
 __global__ void __launch_bounds__(kThreads, 2)
     adapter_down_kernel(const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmDown, const AdapterParams p) {
@@ -290,10 +292,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t n_max = ((uint32_t)(min(per_group, ts.slots) * p.rank) + 15u) & ~15u;
   const uint32_t stage_bytes = kTileBytes + n_max * kRowBytes;
   const uint32_t stages = min((uint32_t)kMaxStages, kRing / stage_bytes);
-  const int32_t pitch = 2 * kBlockK * (p.rank <= kBlockK ? 1 : 2);  // of U's rows
+  const int32_t pitch = P * kBlockK * (p.rank <= kBlockK ? 1 : 2);  // of U's rows
   T* U = static_cast<T*>(p.U) + (int64_t)tile * kAdapterRows * pitch;
-  // value c of a row: 64 at a time, their high parts before their low parts
-  auto place_of = [](int32_t c) { return (c >> 6) * 2 * kBlockK + (c & (kBlockK - 1)); };
+  // value c of a row: 64 at a time, their first parts before their second ones
+  auto place_of = [](int32_t c) { return (c >> 6) * P * kBlockK + (c & (kBlockK - 1)); };
   if (cta == 0 && threadIdx.x < kAdapterRows && ts.slot[threadIdx.x] < 0 &&
       tile * kAdapterRows + (int32_t)threadIdx.x < p.M)
     p.row_scale[tile * kAdapterRows + (int32_t)threadIdx.x] = 0.0f;
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = f * __uint_as_float(v[k]);
             T* dst = U + (int64_t)row * pitch + place_of(c);
-            if (mine) store_parts<T, 8>(dst, dst + kBlockK, o, inv);
+            if (mine) store_parts<T, 8, P>(dst, o, inv);
           }
         }
       }
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int q = 0; q < kQuads; ++q) {
           const int32_t c = (q * 4 + quad) * 4;
           T* dst = U + (int64_t)row * pitch + place_of(c);
-          if (on && c < ((p.rank + 15) & ~15)) store_parts<T, 4>(dst, dst + kBlockK, v[q], inv);
+          if (on && c < ((p.rank + 15) & ~15)) store_parts<T, 4, P>(dst, v[q], inv);
         }
       }
     }
@@ -471,10 +473,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <typename T>
+template <typename T, int P>
 cudaError_t launch(const CUtensorMap& tmX, const CUtensorMap& tmDown, const AdapterParams& p,
                    cudaStream_t stream) {
-  auto kernel = adapter_down_kernel<T>;
+  auto kernel = adapter_down_kernel<T, P>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
@@ -501,8 +503,9 @@ cudaError_t launch(const CUtensorMap& tmX, const CUtensorMap& tmDown, const Adap
 
 cudaError_t launch_adapter_down(const CUtensorMap& tmX, const CUtensorMap& tmDown,
                                 const AdapterParams& p, int elem_in, cudaStream_t stream) {
-  return elem_in == kElemF16 ? launch<__half>(tmX, tmDown, p, stream)
-                             : launch<__nv_bfloat16>(tmX, tmDown, p, stream);
+  if (elem_in == kElemF16) return launch<__half, 2>(tmX, tmDown, p, stream);
+  return p.parts == 3 ? launch<__nv_bfloat16, 3>(tmX, tmDown, p, stream)
+                      : launch<__nv_bfloat16, 2>(tmX, tmDown, p, stream);
 }
 
 }  // namespace gb300

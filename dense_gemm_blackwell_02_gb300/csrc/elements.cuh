@@ -82,6 +82,18 @@ __device__ __forceinline__ void store_f32(T* p, const float (&f)[N]) {
   *reinterpret_cast<Pack<T, N>*>(p) = pack<T, N>(f);
 }
 
+// v as the sum of P parts, each the nearest value to what the parts before it leave (zero
+// after an infinity).
+template <typename T, int P>
+__device__ __forceinline__ void split_f32(float v, T (&part)[P]) {
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    part[j] = from_f32<T>(v);
+    const float f = to_f32(part[j]);
+    v = isinf(f) ? 0.0f : v - f;
+  }
+}
+
 // An index in device memory was out of its range: recorded once, not followed.
 __device__ __forceinline__ void record_bad_index(uint32_t* status, uint32_t site) {
   atomicCAS(status, 0u, (kDevBadIndex << 24) | (site << 16) | (blockIdx.x & 0xFFFFu));

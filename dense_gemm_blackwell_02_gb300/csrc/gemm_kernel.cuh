@@ -611,8 +611,8 @@ struct Layout {
 // holds a CTA (pair) per unit and each running one takes over the work of launches that
 // have not started (ClcLink above).  Grouped launches (whole tiles).
 // ADAPT: low-rank adapters.  The last unit of every tile appends one chain in which each of
-// the tile's adapters multiplies the tile's rows of u (two 16-bit parts, from the kernel
-// before) by its rows of Up, into the accumulator rows that name it and no others
+// the tile's adapters multiplies the tile's rows of u (two or three 16-bit parts, from the
+// kernel before) by its rows of Up, into the accumulator rows that name it and no others
 // (`disable-output-lane`), so that a tile costs 2 rank / 64 K blocks more per adapter and Y
 // is rounded once; the epilogue scales that chain by the row's power of two.  8192 x 10240 x
 // 8192 with 12 adapters of rank 64 in runs of rows: 760 to 785 us with the kernel that
@@ -870,22 +870,22 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
           }
         }
         if constexpr (ADAPT) {
-          // the tile's adapters: u's two parts, each with the adapter's rows of Up
+          // the tile's adapters: u's parts, each with the adapter's rows of Up
           const AdapterTile* at = ad.tiles + w.m_blk;
           grid_dependency_wait();
           const int32_t slots = w.kb1 == p.k_blocks ? __ldg(&at->slots) : 0;
-          const int32_t parts = ad.rank <= kBlockK ? 2 : 4;  // two for every 64 values of u
+          const int32_t blocks = ad.rank <= kBlockK ? ad.parts : 2 * ad.parts;  // of u and of Up
           const CUtensorMap* mapUp = half ? &ad.tmUpHalf : &ad.tmUp;
           for (int32_t e = 0; ok && e < slots; ++e) {
             const int32_t up_row = __ldg(&at->slot[e].adapter) * p.N + b_row;
-            for (int32_t x = 0; x < parts; ++x) {
+            for (int32_t x = 0; x < blocks; ++x) {
               if (!warp_wait_inl(empty_bar(stage), phase ^ 1u, ctl, kSiteEmpty)) {
                 ok = false;
                 break;
               }
               const uint32_t leader_full = mapa_shared(full_bar(stage), group_base);
               if (leader) mbar_arrive_expect_tx_elect(full_bar(stage), tx);
-              tma_load_2d_pair_elect(sB + stage * L::kBBytes, mapUp, (x >> 1) * kBlockK, up_row,
+              tma_load_2d_pair_elect(sB + stage * L::kBBytes, mapUp, x < ad.parts ? 0 : kBlockK, up_row,
                                      leader_full);
               tma_load_2d_pair_elect(sA + stage * L::kABytes, &ad.tmU, x * kBlockK, a_row,
                                      leader_full);
@@ -1026,11 +1026,11 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
               if (!warp_wait_inl(acc_empty_bar(slot), acc_phase ^ 1u, ctl, kSiteAccEmpty)) break;
               tc_fence_after();
               const uint32_t d_tmem = tmem_base + slot * BN;
-              const int32_t parts = ad.rank <= kBlockK ? 2 : 4;
+              const int32_t blocks = ad.rank <= kBlockK ? ad.parts : 2 * ad.parts;
               for (int32_t e = 0; ok && e < slots; ++e) {
                 const uint4 off_lo = __ldg(reinterpret_cast<const uint4*>(at->slot[e].disable));
                 const uint4 off_hi = __ldg(reinterpret_cast<const uint4*>(at->slot[e].disable) + 1);
-                for (int32_t x = 0; x < parts; ++x) {
+                for (int32_t x = 0; x < blocks; ++x) {
                   if (!warp_wait_inl(full_bar(stage), phase, ctl, kSiteFull)) {
                     ok = false;
                     break;
@@ -1039,7 +1039,7 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
                   const uint64_t da = desc_a0 + ((stage * L::kABytes) >> 4);
                   const uint64_t db = desc_b0 + ((stage * L::kBBytes) >> 4);
                   // 16 values of u at a time, as many as the rank has
-                  const int32_t steps = (min(ad.rank - (x >> 1) * kBlockK, kBlockK) + 15) / 16;
+                  const int32_t steps = (min(x < ad.parts ? ad.rank : ad.rank - kBlockK, kBlockK) + 15) / 16;
                   for (int32_t k = 0; k < steps; ++k)
                     umma_pair_masked_elect(d_tmem, da + 2u * (uint32_t)k, db + 2u * (uint32_t)k, idesc,
                                            (x | k) != 0 ? 1u : 0u, off_lo, off_hi);

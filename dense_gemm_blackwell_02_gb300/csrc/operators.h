@@ -118,7 +118,8 @@ struct AdapterParams {
   int32_t ctas;         // CTAs per row tile, a cluster: 1, 2, 4 or 8
   int32_t max_splits;   // K slices at most
   uint32_t idesc;       // instruction descriptor without N, 128 rows
-  void* U;              // M x 128 (rank up to 64) or 256 values of the input type
+  int32_t parts;        // of u (u_parts)
+  void* U;              // M x (64 * parts * ceil(rank / 64)) values of the input type
   float* row_scale;     // M
   AdapterTile* pairs;   // ceil(tiles / 2)
   uint32_t* status;

@@ -172,7 +172,8 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   p.status = h->d_status;
   p.wait_limit_ns = h->wait_limit_ns;
   p.test_stall = h->test_stall;
-  const int64_t pairs = ceil_div(p.tiles, 2), u_cols = 2 * kBlockK * ceil_div(p.rank, kBlockK);
+  p.parts = u_parts(dtype_in == GEMM_BF16, dtype_out == GEMM_F32);
+  const int64_t pairs = ceil_div(p.tiles, 2), u_cols = p.parts * kBlockK * ceil_div(p.rank, kBlockK);
   const size_t u_bytes = round_up((size_t)M * u_cols * 2);
   const size_t scale_bytes = round_up((size_t)M * sizeof(float));
   gemm_status_t st = ensure_scratch(h, u_bytes + scale_bytes + (size_t)pairs * sizeof(AdapterTile), 0);
@@ -193,6 +194,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   g.tiles = p.pairs;
   g.row_scale = p.row_scale;
   g.rank = p.rank;
+  g.parts = p.parts;
   // (the product's configuration is settled before anything is queued)
   return run_adapted(h, X, W, Y, M, N, K, dtype_in, dtype_out, g,
                      [&] { return launch_adapter_down(tmX, tmDown, p, dtype_in, stream); }, stream_);

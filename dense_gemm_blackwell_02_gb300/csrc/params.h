@@ -74,17 +74,26 @@ struct AdapterTile {
   AdapterSlot slot[2 * kBlockM];
 };
 
+// The 16-bit parts whose sum is u, the binary32 intermediate of an adapter, in the second
+// product's operand type.  Each is the nearest to what the ones before leave: after two fp16
+// parts at most 2^-23 of u is left, after two bf16 parts 2^-17, far below the rounding of a
+// 16-bit result, and after three bf16 parts, for binary32 results, nothing.
+__host__ __device__ constexpr int u_parts(bool bf16_in, bool f32_out) {
+  return bf16_in && f32_out ? 3 : 2;
+}
+
 // What an ADAPT kernel takes beside GemmParams; nothing in the others.
 template <bool ADAPT>
 struct AdaptParams {};
 template <>
 struct AdaptParams<true> {
-  CUtensorMap tmU;        // u of every row, M x (128 * chunks): box {64, 128}
+  CUtensorMap tmU;        // u of every row, M x (64 * parts * ceil(rank / 64)): box {64, 128}
   CUtensorMap tmUp;       // (adapters * N) x rank: box {64, BN / 2}
   CUtensorMap tmUpHalf;   // ... box {64, BN / 4} (half-tile units)
   const AdapterTile* tiles;
   const float* row_scale; // M: the factor of each row's term, 0 without an adapter
   int32_t rank;
+  int32_t parts;          // of u (u_parts)
 };
 
 struct GemmParams {
