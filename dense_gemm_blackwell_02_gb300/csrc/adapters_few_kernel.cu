@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
   constexpr int kPitch = RC + 8;  // values per row of a part: rows on different banks
   constexpr int P = u_parts(std::is_same<T, __nv_bfloat16>::value, std::is_same<TO, float>::value);
   __shared__ alignas(16) T part[P][kRows * kPitch];
-  __shared__ float row_scale[kRows];
+  __shared__ float row_scale[kRows];                // NaN for a row whose u has one
+  __shared__ alignas(16) float u_mem[kRows][RC + 4];
   __shared__ float turn[kWarps][8][33];
   const int tid = (int)threadIdx.x, warp = (int)warp_id(), lane = (int)lane_id();
   const int g = lane >> 2, t = lane & 3;
@@ -337,11 +338,15 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
           }
         }
         float big = 0.0f;
+        uint32_t nan = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           v[k] *= scale;
           big = fmaxf(big, fabsf(v[k]));
+          nan |= isnan(v[k]) ? 1u : 0u;
         }
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, off);
         float inv = 1.0f, back = 1.0f;
         if constexpr (std::is_same<T, __half>::value) {
 #pragma unroll
@@ -353,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
           back = __uint_as_float((uint32_t)e << 23);
         }
         if (i < kRows) {
-          if (c == 0) row_scale[i] = back;
+          if (c == 0) row_scale[i] = nan ? __int_as_float(0x7fc00000) : back;
+          store_f32<float, 8>(&u_mem[i][c], v);
           Pack<T, 8> to[P];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -370,6 +376,31 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
     }
     const float s0 = a >= 0 ? row_scale[g] : 0.0f, s1 = a >= 0 ? row_scale[g + 8] : 0.0f;
 
+    auto multiply = [&](const C (&w)[kChunks][4], float (&acc)[4][4]) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int k = (4 * c + t) * kValues;
+        C u0[P], u1[P];
+#pragma unroll
+        for (int s = 0; s < P; ++s) {
+          u0[s] = *reinterpret_cast<const C*>(part[s] + g * kPitch + k);
+          u1[s] = *reinterpret_cast<const C*>(part[s] + (g + 8) * kPitch + k);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int s = 0; s < P; ++s) mma_chunk<T>(acc[j], u0[s], u1[s], w[c][j]);
+      }
+    };
+    // Whether a row's 32 columns have a NaN that u does not have (the four lanes of a row
+    // agree): it comes of an infinity in Up.
+    auto spoilt = [&](const float (&acc)[4][4], int first, float s) {
+      bool nan = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) nan |= isnan(acc[j][first]) || isnan(acc[j][first + 1]);
+      return ((__ballot_sync(0xFFFFFFFFu, nan && s > 0.0f) >> (lane & ~3)) & 0xFu) != 0;
+    };
+    bool again = false;
     for (; q < groups; q += stride) {
       C bn[kChunks][4];
       float on[8];
@@ -381,28 +412,15 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
         }
       }
       float acc[4][4] = {};
-      if (a >= 0) {
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int k = (4 * c + t) * kValues;
-          C u0[P], u1[P];
-#pragma unroll
-          for (int s = 0; s < P; ++s) {
-            u0[s] = *reinterpret_cast<const C*>(part[s] + g * kPitch + k);
-            u1[s] = *reinterpret_cast<const C*>(part[s] + (g + 8) * kPitch + k);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int s = 0; s < P; ++s) mma_chunk<T>(acc[j], u0[s], u1[s], b[c][j]);
-        }
-      }
+      if (a >= 0) multiply(b, acc);
+      const bool skip0 = spoilt(acc, 0, s0), skip1 = spoilt(acc, 2, s1);
+      again |= skip0 || skip1;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         o[2 * j] = fmaf(s0, acc[j][0], o[2 * j]);
         o[2 * j + 1] = fmaf(s0, acc[j][1], o[2 * j + 1]);
       }
-      store(q, row0, o);
+      store(q, skip0 ? -1 : row0, o);
       if (live > 8) {  // rows 8..15 of the group
         load_base(q, row1, o);
 #pragma unroll
@@ -410,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
           o[2 * j] = fmaf(s1, acc[j][2], o[2 * j]);
           o[2 * j + 1] = fmaf(s1, acc[j][3], o[2 * j + 1]);
         }
-        store(q, row1, o);
+        store(q, skip1 ? -1 : row1, o);
       }
       if (q + stride < groups) {
         if constexpr (kAhead) {
@@ -423,6 +441,26 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
         } else {
           load_up(q + stride, b);
           load_base(q + stride, row0, o);
+        }
+      }
+    }
+    // The rows left out, in binary32.
+    if (__any_sync(0xFFFFFFFFu, again)) {
+      for (q = (int)blockIdx.x * kWarps + warp; q < groups; q += stride) {
+        load_up(q, b);
+        float acc[4][4] = {};
+        multiply(b, acc);
+        for (int half = 0; half < 2; ++half) {
+          const int row = half ? row1 : row0;
+          const bool mine = half ? spoilt(acc, 2, s1) : spoilt(acc, 0, s0);
+          if (!__any_sync(0xFFFFFFFFu, mine)) continue;
+          load_base(q, row, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int n = min(q * 32 + 8 * t + k, p.N - 1);
+            if (mine) o[k] += up_times_u(up + (int64_t)n * p.rank, u_mem[g + 8 * half], p.rank);
+          }
+          store(q, mine ? row : -1, o);
         }
       }
     }

@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kThreads = 192;  // warp 0 copies, warp 1 multiplies, warps 2..5 take results out
 constexpr int kMaxStages = 8;
+constexpr float kNan = __builtin_nanf("");
 constexpr uint32_t kRowBytes = 128;                          // 64 values of K
 constexpr uint32_t kTileBytes = kAdapterRows * kRowBytes;    // a 128 x 64 operand tile
 
@@ -385,14 +386,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else {
           // the whole sum: its largest value, then its parts
           float big = 0.0f, inv, back;
+          bool nan = false;
           for (int32_t c = 0; c < p.rank; c += 8) {
             uint32_t v[8];
             tmem_ld_32x32b_x8(at + (uint32_t)c, v);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f * __uint_as_float(v[k])));
+            for (int k = 0; k < 8; ++k) {
+              const float x = f * __uint_as_float(v[k]);
+              big = fmaxf(big, fabsf(x));
+              nan |= isnan(x);
+            }
           }
           row_factors(big, inv, back);
-          if (mine) p.row_scale[tile * kAdapterRows + row] = back;
+          if (mine) p.row_scale[tile * kAdapterRows + row] = nan ? kNan : back;
           // (eight zeros past a rank that is not a multiple of the MMA's 16)
           for (int32_t c = 0; c < ((p.rank + 15) & ~15); c += 8) {
             uint32_t v[8] = {};
@@ -401,6 +407,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = f * __uint_as_float(v[k]);
             T* dst = U + (int64_t)row * pitch + place_of(c);
+            if (mine && c < p.rank)
+              store_f32<float, 8>(p.u + ((int64_t)tile * kAdapterRows + row) * p.rank + c, o);
             if (mine) store_parts<T, 8, P>(dst, o, inv);
           }
         }
@@ -430,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         constexpr int kQuads = kMaxRank / 16;  // of four values, per thread
         float v[kQuads][4];
         float big = 0.0f;
+        uint32_t nan = 0;
 #pragma unroll
         for (int q = 0; q < kQuads; ++q) {
           const int32_t c = (q * 4 + quad) * 4;
@@ -449,14 +458,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int e = 0; e < 4; ++e) {
               v[q][e] *= f;
               big = fmaxf(big, fabsf(v[q][e]));
+              nan |= isnan(v[q][e]) ? 1u : 0u;
             }
+            if (on) store_f32<float, 4>(p.u + ((int64_t)tile * kAdapterRows + row) * p.rank + c, v[q]);
           }
         }
         big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+        nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 1);
+        nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 2);
         float inv, back;
         row_factors(big, inv, back);
-        if (on && quad == 0) p.row_scale[tile * kAdapterRows + row] = back;
+        if (on && quad == 0) p.row_scale[tile * kAdapterRows + row] = nan ? kNan : back;
 #pragma unroll
         for (int q = 0; q < kQuads; ++q) {
           const int32_t c = (q * 4 + quad) * 4;

@@ -94,6 +94,21 @@ __device__ __forceinline__ void split_f32(float v, T (&part)[P]) {
   }
 }
 
+// A row of Up times u, in binary32: what the matrix instructions' sum over the parts of u
+// stands for, except that they make a NaN of an infinity in Up, times parts that are zero or of
+// both signs.
+template <typename T>
+__device__ __forceinline__ float up_times_u(const T* up, const float* u, int32_t rank) {
+  float sum = 0.0f;
+  for (int32_t r = 0; r < rank; r += 8) {
+    float w[8];
+    unpack(*reinterpret_cast<const Pack<T, 8>*>(up + r), w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum = fmaf(u[r + k], w[k], sum);
+  }
+  return sum;
+}
+
 // An index in device memory was out of its range: recorded once, not followed.
 __device__ __forceinline__ void record_bad_index(uint32_t* status, uint32_t site) {
   atomicCAS(status, 0u, (kDevBadIndex << 24) | (site << 16) | (blockIdx.x & 0xFFFFu));

@@ -43,6 +43,7 @@
 
 #include <type_traits>
 
+#include "elements.cuh"
 #include "params.h"
 #include "ptx.cuh"
 #include "umma.cuh"
@@ -579,6 +580,16 @@ struct Layout {
   static_assert((STAGES - 1) * kABytes + kBlockM * kBlockK * 2 <= kRingEnd,
                 "the A operand's 128-row span must stay inside the operand ring");
 };
+
+// (ADAPT, where the matrix instructions do not give it: see the epilogue) column n of row m's
+// adapter term.
+static __device__ __noinline__ float adapter_term(const AdaptParams<true>& ad, int32_t m, int32_t n, int32_t N) {
+  if (n >= N) return 0.0f;
+  const float* u = ad.u + (int64_t)m * ad.rank;
+  const int64_t at = ((int64_t)ad.row_adapter[m] * N + n) * ad.rank;
+  return ad.bf16 ? up_times_u(static_cast<const __nv_bfloat16*>(ad.up) + at, u, ad.rank)
+                 : up_times_u(static_cast<const __half*>(ad.up) + at, u, ad.rank);
+}
 
 // ONE_CHAIN: every work unit is a single accumulation chain (at most p.chain_kb
 // k-blocks), so the epilogue streams the accumulator out of TMEM in 32-column pieces
@@ -1246,12 +1257,13 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
       const int32_t base_chains = chains_of(w, p.chain_kb);
       int32_t nchains = base_chains;
       float row_factor = 0.0f;  // (ADAPT) of this thread's row in the adapters' chain
+      uint32_t redo = 0;        // (ADAPT) bit pc: the row's adapter term there is not the MMAs'
+      const int32_t my_m = w.m_blk * kRowsTile + (int32_t)rank * rows_cta + (int32_t)row;
       if constexpr (ADAPT) {
         grid_dependency_wait();
         if (w.kb1 == p.k_blocks && __ldg(&ad.tiles[w.m_blk].slots) > 0) {
           ++nchains;
-          const int32_t m = w.m_blk * kRowsTile + (int32_t)rank * rows_cta + (int32_t)row;
-          if (m < p.M) row_factor = __ldg(ad.row_scale + m);
+          if (my_m < p.M) row_factor = __ldg(ad.row_scale + my_m);
         }
       }
       if constexpr (KIND == 2) {
@@ -1390,8 +1402,14 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[32 * pc + j] = __uint_as_float(r[j]);
               } else if (ADAPT && ch >= base_chains) {
-                // rows without an adapter: lanes no MMA wrote
-                if (row_factor != 0.0f) {
+                // rows without an adapter: lanes no MMA wrote.  A NaN where u has none comes
+                // of an infinity in Up.
+                bool nan = false;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) nan |= isnan(__uint_as_float(r[j]));
+                if (nan && row_factor > 0.0f) {
+                  redo |= 1u << pc;
+                } else if (row_factor != 0.0f) {
 #pragma unroll
                   for (int j = 0; j < 32; ++j)
                     acc[32 * pc + j] = fmaf(row_factor, __uint_as_float(r[j]), acc[32 * pc + j]);
@@ -1419,6 +1437,25 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
       const int32_t m0 = w.m_blk * kRowsTile + (int32_t)rank * rows_cta;  // first row of this CTA
       // first column written by this warp
       const int32_t n_half = w.n_blk * BN + (w.half >= 0 ? w.half : (int32_t)h) * kHalf;
+      if constexpr (ADAPT) {
+        if (__any_sync(0xFFFFFFFFu, redo != 0)) {
+#pragma unroll
+          for (int pc = 0; pc < kPieces; ++pc) {
+            // row after row, a column per lane
+            uint32_t rows = __ballot_sync(0xFFFFFFFFu, (redo >> pc) & 1u);
+            for (; rows != 0; rows &= rows - 1) {
+              const int src = __ffs((int)rows) - 1;
+              const float v = adapter_term(ad, __shfl_sync(0xFFFFFFFFu, my_m, src),
+                                           n_half + 32 * pc + (int32_t)lane, p.N);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float x = __shfl_sync(0xFFFFFFFFu, v, j);
+                if ((int)lane == src) acc[32 * pc + j] += x;
+              }
+            }
+          }
+        }
+      }
       bool exchanged = false;
       if constexpr (KX2) {
         if (w.nsplit > 1) {

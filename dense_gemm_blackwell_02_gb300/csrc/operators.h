@@ -121,6 +121,7 @@ struct AdapterParams {
   int32_t parts;        // of u (u_parts)
   void* U;              // M x (64 * parts * ceil(rank / 64)) values of the input type
   float* row_scale;     // M
+  float* u;             // M x rank
   AdapterTile* pairs;   // ceil(tiles / 2)
   uint32_t* status;
   uint64_t wait_limit_ns;

@@ -176,12 +176,15 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   const int64_t pairs = ceil_div(p.tiles, 2), u_cols = p.parts * kBlockK * ceil_div(p.rank, kBlockK);
   const size_t u_bytes = round_up((size_t)M * u_cols * 2);
   const size_t scale_bytes = round_up((size_t)M * sizeof(float));
-  gemm_status_t st = ensure_scratch(h, u_bytes + scale_bytes + (size_t)pairs * sizeof(AdapterTile), 0);
+  const size_t pair_bytes = round_up((size_t)pairs * sizeof(AdapterTile));
+  gemm_status_t st = ensure_scratch(
+      h, u_bytes + scale_bytes + pair_bytes + (size_t)M * p.rank * sizeof(float), 0);
   if (st != GEMM_OK) return st;
   char* scratch = static_cast<char*>(h->op.ptr);
   p.U = scratch;
   p.row_scale = reinterpret_cast<float*>(scratch + u_bytes);
   p.pairs = reinterpret_cast<AdapterTile*>(scratch + u_bytes + scale_bytes);
+  p.u = reinterpret_cast<float*>(scratch + u_bytes + scale_bytes + pair_bytes);
 
   CUtensorMap tmX, tmDown;
   AdaptParams<true> g;
@@ -193,6 +196,10 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     return GEMM_ERR_CUDA;
   g.tiles = p.pairs;
   g.row_scale = p.row_scale;
+  g.u = p.u;
+  g.up = ad->up;
+  g.row_adapter = row_adapter;
+  g.bf16 = dtype_in == GEMM_BF16;
   g.rank = p.rank;
   g.parts = p.parts;
   // (the product's configuration is settled before anything is queued)

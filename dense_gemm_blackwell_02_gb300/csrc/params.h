@@ -77,7 +77,9 @@ struct AdapterTile {
 // The 16-bit parts whose sum is u, the binary32 intermediate of an adapter, in the second
 // product's operand type.  Each is the nearest to what the ones before leave: after two fp16
 // parts at most 2^-23 of u is left, after two bf16 parts 2^-17, far below the rounding of a
-// 16-bit result, and after three bf16 parts, for binary32 results, nothing.
+// 16-bit result, and after three bf16 parts, for binary32 results, nothing.  (Parts of one sign,
+// none of them zero, would keep infinities in Up as they are; but the matrix instructions'
+// sums truncate, and such parts made even sums of small integers inexact.)
 __host__ __device__ constexpr int u_parts(bool bf16_in, bool f32_out) {
   return bf16_in && f32_out ? 3 : 2;
 }
@@ -91,9 +93,13 @@ struct AdaptParams<true> {
   CUtensorMap tmUp;       // (adapters * N) x rank: box {64, BN / 2}
   CUtensorMap tmUpHalf;   // ... box {64, BN / 4} (half-tile units)
   const AdapterTile* tiles;
-  const float* row_scale; // M: the factor of each row's term, 0 without an adapter
+  const float* row_scale; // M: the factor of each row's term, 0 without an adapter, NaN if u has one
+  const float* u;         // M x rank
+  const void* up;
+  const int32_t* row_adapter;
   int32_t rank;
   int32_t parts;          // of u (u_parts)
+  int32_t bf16;           // Up's type: bf16 or fp16
 };
 
 struct GemmParams {

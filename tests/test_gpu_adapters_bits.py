@@ -78,3 +78,77 @@ def test_binary32_results_have_every_bit_of_u_with_bf16_inputs(g, M, R):
     u = u * torch.where(ids >= 0, scale[ids.clamp(min=0).long()], torch.ones(())).double()[:, None]
     got = _run(g, X, down, up, ids, torch.float32, scale=scale)
     assert torch.equal(got.double(), _columns(u, power, ids, up.shape[1]))
+
+
+@BOTH
+@pytest.mark.parametrize("R", [8, 24, 64, 128])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("out", ["same", torch.float32])
+def test_infinities_in_up_give_what_the_formula_gives(g, M, R, dt, out):
+    # small integers, so that every finite sum is exact and each result is the formula's
+    # value rounded once; u is often zero, often exact in one part and of either sign
+    out = dt if out == "same" else out
+    gen = torch.Generator().manual_seed(M + 3 * R)
+    K, N, L = 64, 300, 6
+    X = torch.randint(-3, 4, (M, K), generator=gen).to(dt)
+    X[::7, 8:] = 0
+    down = torch.randint(-2, 3, (L, R, K), generator=gen).to(dt)
+    down[:, 1] = torch.randint(-120, 121, (L, K), generator=gen).to(dt)
+    up = torch.randint(-2, 3, (L, N, R), generator=gen).to(dt)
+    inf = float("inf")
+    up[0, 0, 0], up[0, 40, 1], up[0, 299, R - 1] = inf, -inf, inf
+    up[1, 7, 0], up[1, 7, 3] = inf, -inf               # of one or of both signs, by u
+    up[2, 130, :] = inf
+    up[3, 64:70, 2] = -inf
+    up[3, 65, 5] = float("nan")
+    ids = torch.randint(-1, L, (M,), generator=gen, dtype=torch.int32)
+    W = torch.randint(-2, 3, (N, K), generator=gen).to(dt)
+    u = _u(X, down, ids)
+    assert u.abs().max() < 2 ** 16 and (u == 0).any()
+    want = X.double() @ W.double().T
+    for a in range(L):
+        r = ids == a
+        want[r] += (u[r][:, None, :] * up[a].double()).sum(-1)
+    finite = want[torch.isfinite(want)]
+    assert finite.abs().max() < 2 ** 24 and want.isinf().any() and want.isnan().any()
+    Y = torch.full((M, N), 7.0, dtype=out, device="cuda")
+    g.run_adapters(X.cuda(), W.cuda(), Y, down.cuda(), up.cuda(), ids.cuda())
+    torch.cuda.synchronize()
+    got, want = Y.cpu(), want.float().to(out)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(nan=0.0, posinf=inf, neginf=-inf),
+                       want.nan_to_num(nan=0.0, posinf=inf, neginf=-inf))
+
+
+@BOTH
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_infinities_and_nan_in_x_give_what_the_formula_gives(g, M, dt):
+    # u of row 5 has infinities, row 9's has NaN; two values of the others are infinite
+    gen = torch.Generator().manual_seed(M)
+    K, N, R, L = 64, 130, 16, 3
+    X = torch.randint(-3, 4, (M, K), generator=gen).to(dt)
+    down = torch.randint(-2, 3, (L, R, K), generator=gen).to(dt)
+    down[:, :, 5] = 0
+    down[:, 2, 5], down[:, 3, 5] = 1, -1
+    up = torch.randint(-2, 3, (L, N, R), generator=gen).to(dt)
+    up[:, :, 2] = torch.randint(1, 3, (L, N), generator=gen).to(dt)
+    up[:, :60, 3] = 0                                   # infinity times zero: NaN
+    up[:, 60:, 3] = -1
+    up[1, 100, 4] = float("inf")
+    ids = torch.randint(0, L, (M,), generator=gen, dtype=torch.int32)
+    ids[5], ids[9] = 1, 2
+    X[5, 5], X[9, 5] = float("inf"), float("nan")
+    u = torch.stack([(down[int(a)].double() * x.double()).sum(-1) for a, x in zip(ids, X)])
+    # (infinity times the zeros of Down: NaN in every other value of u, as the formula has it)
+    want = torch.stack([(up[int(a)].double() * v).sum(-1) for a, v in zip(ids, u)])
+    Y = torch.full((M, N), 7.0, dtype=torch.float32, device="cuda")
+    g.run_adapters(X.cuda(), torch.zeros(N, K, dtype=dt, device="cuda"), Y, down.cuda(), up.cuda(),
+                   ids.cuda())
+    torch.cuda.synchronize()
+    got = Y.cpu()
+    rows = torch.ones(M, dtype=torch.bool)
+    rows[[5, 9]] = False
+    assert torch.isnan(got[[5, 9]]).all() and torch.isnan(want[[5, 9]]).all()
+    same = got[rows].double() == want[rows]
+    both = torch.isnan(got[rows]) & torch.isnan(want[rows])
+    assert (same | both).all()
