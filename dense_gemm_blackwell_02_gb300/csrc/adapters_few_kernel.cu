@@ -224,9 +224,7 @@ __host__ __device__ constexpr int up_ctas_per_sm(int rc) { return rc <= 16 ? 6 :
 
 // Grid: x a share of Y's columns, y the group.  RC: the rank's class, 16, 32, 64 or 128.  A
 // warp takes 32 columns at a time, and loads the next ones' weights and base before it
-// multiplies the present ones'.  u enters the MMA as 16-bit parts, u = 2^e (first + second
-// ...), e the exponent of the row's largest value in fp16 (whose range would cut u off) and 0
-// in bf16.
+// multiplies the present ones'.  u enters the MMA as 16-bit parts (row_factor, split_f32).
 template <typename T, typename TO, int RC>
 __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
     few_up_kernel(const __grid_constant__ AdapterFewParams p) {
@@ -236,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
   constexpr int kPitch = RC + 8;  // values per row of a part: rows on different banks
   constexpr int P = u_parts(std::is_same<T, __nv_bfloat16>::value, std::is_same<TO, float>::value);
   __shared__ alignas(16) T part[P][kRows * kPitch];
-  __shared__ float row_scale[kRows];                // NaN for a row whose u has one
+  __shared__ float row_scale[kRows];  // (RowFactor)
   __shared__ alignas(16) float u_mem[kRows][RC + 4];
   __shared__ float turn[kWarps][8][33];
   const int tid = (int)threadIdx.x, warp = (int)warp_id(), lane = (int)lane_id();
@@ -337,39 +335,28 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
             }
           }
         }
-        float big = 0.0f;
-        uint32_t nan = 0;
+        RowRange range;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           v[k] *= scale;
-          big = fmaxf(big, fabsf(v[k]));
-          nan |= isnan(v[k]) ? 1u : 0u;
+          range.add(v[k]);
         }
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, off);
-        float inv = 1.0f, back = 1.0f;
-        if constexpr (std::is_same<T, __half>::value) {
-#pragma unroll
-          for (int off = kLanes / 2; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, off));
-          int32_t e = (int32_t)(__float_as_uint(big) >> 23);
-          if (e == 0 || e == 255) e = 127;  // zero, infinities, NaN: unscaled
-          e = min(max(e, 2), 252);
-          inv = __uint_as_float((uint32_t)(254 - e) << 23);
-          back = __uint_as_float((uint32_t)e << 23);
-        }
+        range.join(kLanes);
+        const RowFactor to = row_factor<T>(range, std::is_same<TO, float>::value);
         if (i < kRows) {
-          if (c == 0) row_scale[i] = nan ? __int_as_float(0x7fc00000) : back;
+          if (c == 0) row_scale[i] = to.scale;
           store_f32<float, 8>(&u_mem[i][c], v);
-          Pack<T, 8> to[P];
+          Pack<T, 8> x8[P];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             T x[P];
-            split_f32(v[k] * inv, x);
+            // (a row with a NaN has NaN for its factor; its parts need not make more of them)
+            split_f32(isnan(to.scale) ? 0.0f : v[k] * to.inv, x);
 #pragma unroll
-            for (int j = 0; j < P; ++j) to[j].v[k] = x[j];
+            for (int j = 0; j < P; ++j) x8[j].v[k] = x[j];
           }
 #pragma unroll
-          for (int j = 0; j < P; ++j) *reinterpret_cast<Pack<T, 8>*>(part[j] + i * kPitch + c) = to[j];
+          for (int j = 0; j < P; ++j) *reinterpret_cast<Pack<T, 8>*>(part[j] + i * kPitch + c) = x8[j];
         }
       }
       __syncthreads();
@@ -392,13 +379,18 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
           for (int s = 0; s < P; ++s) mma_chunk<T>(acc[j], u0[s], u1[s], w[c][j]);
       }
     };
-    // Whether a row's 32 columns have a NaN that u does not have (the four lanes of a row
-    // agree): it comes of an infinity in Up.
-    auto spoilt = [&](const float (&acc)[4][4], int first, float s) {
-      bool nan = false;
+    // Whether the warp's 32 columns have to be looked at again: the parts do not hold one of the
+    // rows, or there is an infinity or a NaN (times zero: NaN).  One vote; two, one for each
+    // half of the rows, cost the kernel 1 us in 10.
+    const bool wide = s0 < 0.0f || s1 < 0.0f;
+    auto look_again = [&](const float (&acc)[4][4]) {
+      float z0 = 0.0f, z1 = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) nan |= isnan(acc[j][first]) || isnan(acc[j][first + 1]);
-      return ((__ballot_sync(0xFFFFFFFFu, nan && s > 0.0f) >> (lane & ~3)) & 0xFu) != 0;
+      for (int j = 0; j < 4; ++j) {
+        fma2_rn(z0, z1, acc[j][0], acc[j][1], 0.0f);
+        fma2_rn(z0, z1, acc[j][2], acc[j][3], 0.0f);
+      }
+      return __any_sync(0xFFFFFFFFu, z0 + z1 != 0.0f || wide) != 0;
     };
     bool again = false;
     for (; q < groups; q += stride) {
@@ -413,22 +405,22 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
       }
       float acc[4][4] = {};
       if (a >= 0) multiply(b, acc);
-      const bool skip0 = spoilt(acc, 0, s0), skip1 = spoilt(acc, 2, s1);
-      again |= skip0 || skip1;
+      const bool skip = look_again(acc);
+      again |= skip;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         o[2 * j] = fmaf(s0, acc[j][0], o[2 * j]);
         o[2 * j + 1] = fmaf(s0, acc[j][1], o[2 * j + 1]);
       }
-      store(q, skip0 ? -1 : row0, o);
-      if (live > 8) {  // rows 8..15 of the group
+      if (!skip) store(q, row0, o);
+      if (live > 8 && !skip) {  // rows 8..15 of the group
         load_base(q, row1, o);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           o[2 * j] = fmaf(s1, acc[j][2], o[2 * j]);
           o[2 * j + 1] = fmaf(s1, acc[j][3], o[2 * j + 1]);
         }
-        store(q, skip1 ? -1 : row1, o);
+        store(q, row1, o);
       }
       if (q + stride < groups) {
         if constexpr (kAhead) {
@@ -444,23 +436,28 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
         }
       }
     }
-    // The rows left out, in binary32.
-    if (__any_sync(0xFFFFFFFFu, again)) {
+    // The columns left out: rows that the parts do not hold, and what is not finite, in binary32.
+    if (again) {
       for (q = (int)blockIdx.x * kWarps + warp; q < groups; q += stride) {
         load_up(q, b);
         float acc[4][4] = {};
         multiply(b, acc);
+        if (!look_again(acc)) continue;
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int row = half ? row1 : row0;
-          const bool mine = half ? spoilt(acc, 2, s1) : spoilt(acc, 0, s0);
-          if (!__any_sync(0xFFFFFFFFu, mine)) continue;
+          const float s = half ? s1 : s0;
           load_base(q, row, o);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
+            const float x = acc[k / 2][2 * half + k % 2];
             const int n = min(q * 32 + 8 * t + k, p.N - 1);
-            if (mine) o[k] += up_times_u(up + (int64_t)n * p.rank, u_mem[g + 8 * half], p.rank);
+            if (s < 0.0f || (s > 0.0f && !(fabsf(x) < __builtin_huge_valf())))
+              o[k] += up_times_u(up + (int64_t)n * p.rank, u_mem[g + 8 * half], p.rank);
+            else
+              o[k] = fmaf(s, x, o[k]);
           }
-          store(q, mine ? row : -1, o);
+          store(q, row, o);
         }
       }
     }

@@ -19,9 +19,10 @@
 // u take the rest: the latency of its steps bounds it, not X's 17 MB.  Asking for X ahead of
 // the rows' adapters (into L2) delays the first K block by 2 us.
 //
-// u leaves as 16-bit parts, u = 2^e (first + second ...) with e the exponent of the row's
-// largest value, which brings them into fp16's range: one part alone would round u to 8 or 11
-// bits, an error of the size of Y's own rounding (how many, and what they leave: u_parts).
+// u leaves as 16-bit parts, in fp16 times a power of two that brings the row into its range
+// (row_factor): one part alone would round u to 8 or 11 bits, an error of the size of Y's own
+// rounding (how many, and what they leave: u_parts).  u itself goes along in binary32 for the
+// rows and columns that parts do not serve.
 #include <algorithm>
 
 #include "elements.cuh"
@@ -36,7 +37,6 @@ namespace {
 
 constexpr int kThreads = 192;  // warp 0 copies, warp 1 multiplies, warps 2..5 take results out
 constexpr int kMaxStages = 8;
-constexpr float kNan = __builtin_nanf("");
 constexpr uint32_t kRowBytes = 128;                          // 64 values of K
 constexpr uint32_t kTileBytes = kAdapterRows * kRowBytes;    // a 128 x 64 operand tile
 
@@ -158,16 +158,6 @@ constexpr int kNumBars = 2 * kMaxStages + 3;
 // CTA of a group adds its share of the rows, in slice order.
 constexpr uint32_t kRing = 96 * 1024;  // two CTAs per SM
 constexpr uint32_t kSmem = kRing + 1024;
-
-// u = 2^e (hi + lo) of `n` values of a row whose largest magnitude is `big`: the factor that
-// brings it near 1 and its inverse; 1 for zero, infinities and NaN (which pass through).
-__device__ __forceinline__ void row_factors(float big, float& inv, float& back) {
-  int32_t e = (int32_t)(__float_as_uint(big) >> 23);
-  if (e == 0 || e == 255) e = 127;
-  e = min(max(e, 2), 252);
-  inv = __uint_as_float((uint32_t)(254 - e) << 23);
-  back = __uint_as_float((uint32_t)e << 23);
-}
 
 // N values times inv as P parts, kBlockK values apart.
 template <typename T, int N, int P>
@@ -384,21 +374,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
         } else {
-          // the whole sum: its largest value, then its parts
-          float big = 0.0f, inv, back;
-          bool nan = false;
+          // the whole sum: its range, then its parts
+          RowRange range;
           for (int32_t c = 0; c < p.rank; c += 8) {
             uint32_t v[8];
             tmem_ld_32x32b_x8(at + (uint32_t)c, v);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float x = f * __uint_as_float(v[k]);
-              big = fmaxf(big, fabsf(x));
-              nan |= isnan(x);
-            }
+            for (int k = 0; k < 8; ++k) range.add(f * __uint_as_float(v[k]));
           }
-          row_factors(big, inv, back);
-          if (mine) p.row_scale[tile * kAdapterRows + row] = nan ? kNan : back;
+          const RowFactor to = row_factor<T>(range, p.f32_out);
+          if (mine) p.row_scale[tile * kAdapterRows + row] = to.scale;
           // (eight zeros past a rank that is not a multiple of the MMA's 16)
           for (int32_t c = 0; c < ((p.rank + 15) & ~15); c += 8) {
             uint32_t v[8] = {};
@@ -409,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             T* dst = U + (int64_t)row * pitch + place_of(c);
             if (mine && c < p.rank)
               store_f32<float, 8>(p.u + ((int64_t)tile * kAdapterRows + row) * p.rank + c, o);
-            if (mine) store_parts<T, 8, P>(dst, o, inv);
+            if (mine) store_parts<T, 8, P>(dst, o, to.inv);
           }
         }
       }
@@ -437,8 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t src = ring + (uint32_t)(row * (p.rank + 4)) * 4u;
         constexpr int kQuads = kMaxRank / 16;  // of four values, per thread
         float v[kQuads][4];
-        float big = 0.0f;
-        uint32_t nan = 0;
+        RowRange range;
 #pragma unroll
         for (int q = 0; q < kQuads; ++q) {
           const int32_t c = (q * 4 + quad) * 4;
@@ -457,24 +441,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               v[q][e] *= f;
-              big = fmaxf(big, fabsf(v[q][e]));
-              nan |= isnan(v[q][e]) ? 1u : 0u;
+              range.add(v[q][e]);
             }
             if (on) store_f32<float, 4>(p.u + ((int64_t)tile * kAdapterRows + row) * p.rank + c, v[q]);
           }
         }
-        big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-        nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 1);
-        nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 2);
-        float inv, back;
-        row_factors(big, inv, back);
-        if (on && quad == 0) p.row_scale[tile * kAdapterRows + row] = nan ? kNan : back;
+        range.join(4);
+        const RowFactor to = row_factor<T>(range, p.f32_out);
+        if (on && quad == 0) p.row_scale[tile * kAdapterRows + row] = to.scale;
 #pragma unroll
         for (int q = 0; q < kQuads; ++q) {
           const int32_t c = (q * 4 + quad) * 4;
           T* dst = U + (int64_t)row * pitch + place_of(c);
-          if (on && c < ((p.rank + 15) & ~15)) store_parts<T, 4, P>(dst, v[q], inv);
+          if (on && c < ((p.rank + 15) & ~15)) store_parts<T, 4, P>(dst, v[q], to.inv);
         }
       }
     }

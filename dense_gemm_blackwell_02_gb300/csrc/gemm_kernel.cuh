@@ -1264,6 +1264,7 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
         if (w.kb1 == p.k_blocks && __ldg(&ad.tiles[w.m_blk].slots) > 0) {
           ++nchains;
           if (my_m < p.M) row_factor = __ldg(ad.row_scale + my_m);
+          if (row_factor < 0.0f) redo = (1u << kPieces) - 1u, row_factor = 0.0f;
         }
       }
       if constexpr (KIND == 2) {
@@ -1402,12 +1403,18 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[32 * pc + j] = __uint_as_float(r[j]);
               } else if (ADAPT && ch >= base_chains) {
-                // rows without an adapter: lanes no MMA wrote.  A NaN where u has none comes
-                // of an infinity in Up.
-                bool nan = false;
+                // (rows without an adapter: lanes no MMA wrote)
+                bool finite = true;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) nan |= isnan(__uint_as_float(r[j]));
-                if (nan && row_factor > 0.0f) {
+                for (int j = 0; j < 32; ++j) finite &= fabsf(__uint_as_float(r[j])) < __builtin_huge_valf();
+                if (!finite) {  // (columns past N are the next adapter's)
+                  const int32_t n0 = w.n_blk * BN + (w.half >= 0 ? w.half : (int32_t)h) * kHalf + 32 * pc;
+                  finite = true;
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    finite &= fabsf(__uint_as_float(r[j])) < __builtin_huge_valf() || n0 + j >= p.N;
+                }
+                if (!finite && row_factor > 0.0f) {
                   redo |= 1u << pc;
                 } else if (row_factor != 0.0f) {
 #pragma unroll

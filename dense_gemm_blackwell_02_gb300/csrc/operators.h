@@ -119,8 +119,9 @@ struct AdapterParams {
   int32_t max_splits;   // K slices at most
   uint32_t idesc;       // instruction descriptor without N, 128 rows
   int32_t parts;        // of u (u_parts)
+  int32_t f32_out;      // Y's type is binary32
   void* U;              // M x (64 * parts * ceil(rank / 64)) values of the input type
-  float* row_scale;     // M
+  float* row_scale;     // M (RowFactor)
   float* u;             // M x rank
   AdapterTile* pairs;   // ceil(tiles / 2)
   uint32_t* status;

@@ -172,6 +172,7 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   p.status = h->d_status;
   p.wait_limit_ns = h->wait_limit_ns;
   p.test_stall = h->test_stall;
+  p.f32_out = dtype_out == GEMM_F32;
   p.parts = u_parts(dtype_in == GEMM_BF16, dtype_out == GEMM_F32);
   const int64_t pairs = ceil_div(p.tiles, 2), u_cols = p.parts * kBlockK * ceil_div(p.rank, kBlockK);
   const size_t u_bytes = round_up((size_t)M * u_cols * 2);

@@ -93,7 +93,7 @@ struct AdaptParams<true> {
   CUtensorMap tmUp;       // (adapters * N) x rank: box {64, BN / 2}
   CUtensorMap tmUpHalf;   // ... box {64, BN / 4} (half-tile units)
   const AdapterTile* tiles;
-  const float* row_scale; // M: the factor of each row's term, 0 without an adapter, NaN if u has one
+  const float* row_scale; // M: of each row's term (RowFactor), 0 without an adapter
   const float* u;         // M x rank
   const void* up;
   const int32_t* row_adapter;

@@ -443,8 +443,9 @@ gemm_status_t gemm_run_noalloc(const void* A, const void* B, void* C, int64_t M,
  * An adapter's values reach only the rows that name it: infinities or NaN in one
  * adapter leave the other rows as they are.
  * Down . X and the sum of both terms are held in binary32, and Y is rounded once.  Down . X
- * enters the second product exactly with bf16 inputs and binary32 results, to within 2^-23 of
- * it with fp16 inputs, and to within 2^-17 with bf16 inputs and 16-bit results.
+ * enters the second product exactly with bf16 inputs and binary32 results, to within 2^-20 of
+ * every value (2^-23 of those within 2^16 of the row's largest) with fp16 inputs and binary32
+ * results, and to within 2^-17 of every value with 16-bit results.
  */
 typedef struct {
   const void* down;

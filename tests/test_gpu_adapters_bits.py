@@ -152,3 +152,116 @@ def test_infinities_and_nan_in_x_give_what_the_formula_gives(g, M, dt):
     same = got[rows].double() == want[rows]
     both = torch.isnan(got[rows]) & torch.isnan(want[rows])
     assert (same | both).all()
+
+
+def _powers(M, R, L, dt, low, high, gen):
+    """X, Down and ids whose u[i][r] is one product of two values of their type, of a size
+    between 2^low and 2^high (both reached in most rows), by one value other than zero in
+    every row of Down."""
+    K = 8 * ((R + 7) // 8)
+    ids = torch.randint(0, L, (M,), generator=gen, dtype=torch.int32)
+    half = torch.randint(low // 2, high // 2 + 1, (L, R), generator=gen)
+    half[:, 0], half[:, 1] = high // 2, low // 2
+    at = torch.stack([torch.randperm(K, generator=gen)[:R] for _ in range(L)])
+    down = torch.zeros(L, R, K)
+    down.scatter_(2, at[:, :, None], ((1 + torch.rand(L, R, generator=gen)) * 2.0 ** half)[:, :, None])
+    X = torch.zeros(M, K)
+    X.scatter_(1, at[ids.long()], 2.0 ** half[ids.long()] * (1 + torch.rand(M, R, generator=gen))
+               * (1 - 2 * torch.randint(0, 2, (M, R), generator=gen)))
+    return X.to(dt), down.to(dt), ids
+
+
+def _each_value(g, X, down, ids, R, out, relative):
+    """Every column of Y is u's value times a power of two to within `relative` of it, and a
+    rounding."""
+    N = 300
+    up, power = _single(len(down), N, R, X.dtype)
+    u = _u(X, down, ids)
+    want = _columns(u, power, ids, N)
+    got = _run(g, X, down, up, ids, out).double()
+    ulp = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[out]
+    # rows whose u binary32 holds, and what it holds of their results (past its end: infinity)
+    end = 2.0 ** 128 * (1 - 2.0 ** -25)
+    rows = (u.abs() < end).all(dim=1)
+    got, want = got[rows], want[rows]
+    over = want.abs() >= end
+    assert rows.any() and (got[over] == want[over].sign() * float("inf")).all()
+    got, want = got[~over], want[~over]
+    assert ((got - want).abs() <= (relative + ulp * (1 + relative)) * want.abs()).all()
+    return u
+
+
+@BOTH
+@RANKS
+@pytest.mark.parametrize("out,relative", [(torch.float32, 2.0 ** -20), (torch.bfloat16, 2.0 ** -17)])
+@pytest.mark.parametrize("low,high", [(-24, 20), (-8, 18), (-28, -10), (4, 22)])
+def test_values_far_below_their_rows_largest_survive_in_fp16(g, M, R, out, relative, low, high):
+    X, down, ids = _powers(M, R, 5, torch.float16, low, high, torch.Generator().manual_seed(R + M + high))
+    u = _each_value(g, X, down, ids, R, out, relative)
+    assert u.abs().max() / u[u != 0].abs().min() > 2.0 ** (high - low - 2)
+
+
+@BOTH
+@RANKS
+@pytest.mark.parametrize("low,high", [(-124, -80), (-120, 60), (-60, 120), (90, 126)])
+def test_binary32_results_have_every_value_of_u_with_bf16_inputs(g, M, R, low, high):
+    X, down, ids = _powers(M, R, 5, torch.bfloat16, low, high, torch.Generator().manual_seed(R + M + high))
+    _each_value(g, X, down, ids, R, torch.float32, 0.0)
+
+
+@BOTH
+def test_large_values_in_up_with_bf16_inputs(g, M):
+    # Up of 2^126 times u of 2^-30: eight such terms are far from binary32's end
+    K, N, R, L = 64, 130, 8, 2
+    X = torch.zeros(M, K).bfloat16()
+    X[:, 0] = 2.0 ** -15
+    down = torch.zeros(L, R, K).bfloat16()
+    down[:, :, 0] = 2.0 ** -15
+    up = torch.full((L, N, R), 2.0 ** 126).bfloat16()
+    ids = torch.zeros(M, dtype=torch.int32)
+    for out in (torch.float32, torch.bfloat16):
+        assert (_run(g, X, down, up, ids, out) == 8 * 2.0 ** 96).all()
+
+
+def test_a_row_with_one_wide_value_leaves_the_other_rows_bits(g):
+    # (the row is multiplied in binary32, its neighbours in the tensor cores as before)
+    for M in (40, 700):
+        gen = torch.Generator().manual_seed(M)
+        X = torch.randn(M, 256, generator=gen).half()
+        down = (torch.randn(3, 16, 256, generator=gen) / 16).half()
+        up = torch.randn(3, 200, 16, generator=gen).half()
+        ids = torch.randint(0, 3, (M,), generator=gen, dtype=torch.int32)
+        before = _run(g, X, down, up, ids, torch.float32)
+        X[7] = 0
+        X[7, 0] = 2.0 ** -24
+        down[:, :, 0], down[:, 0, 0] = 2.0 ** -10, 2.0 ** 15
+        X2 = X.clone()
+        X2[:, 0] = 0
+        X2[7, 0] = X[7, 0]
+        rows = torch.arange(M) != 7
+        a = _run(g, X2, down, up, ids, torch.float32)
+        X2[7, 0] = 0
+        b = _run(g, X2, down, up, ids, torch.float32)
+        assert torch.equal(a[rows], b[rows]) and (b[7] == 0).all()
+        u = _u(X, down, ids)[7]
+        want = (up[ids[7].item()].double() * u).sum(-1)
+        mag = (up[ids[7].item()].double() * u).abs().sum(-1)
+        assert ((a[7].double() - want).abs() <= 17 * 2.0 ** -24 * mag).all()
+        assert torch.isfinite(before).all()
+
+
+def test_an_infinity_at_the_start_of_one_adapter_leaves_the_end_of_the_one_before(g):
+    # (in the tiles, columns past N meet the next adapter's rows of Up)
+    gen = torch.Generator().manual_seed(17)
+    for M in (40, 900):
+        X = torch.randn(M, 256, generator=gen).bfloat16()
+        down = (torch.randn(4, 16, 256, generator=gen) / 16).bfloat16()
+        up = torch.randn(4, 300, 16, generator=gen).bfloat16()
+        ids = torch.randint(0, 4, (M,), generator=gen, dtype=torch.int32)
+        for out in (torch.bfloat16, torch.float32):
+            before = _run(g, X, down, up, ids, out)
+            spoilt = up.clone()
+            spoilt[1:, :6] = float("inf")
+            got = _run(g, X, down, spoilt, ids, out)
+            assert torch.equal(got[ids == 0], before[ids == 0])
+            assert torch.equal(got[:, 32:], before[:, 32:])
