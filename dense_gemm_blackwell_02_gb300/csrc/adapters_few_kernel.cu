@@ -105,9 +105,11 @@ __device__ __forceinline__ void few_down_unit(const AdapterFewParams& p, int row
     int at = lane == 0 ? (int)atomicAdd(p.counts, 1u) : 0;
     at = __shfl_sync(0xFFFFFFFFu, at, 0);
     const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine >= 0));
-    FewGroup& entry = p.groups[at];
-    if (lane < kRows) entry.row[lane] = mine;
-    if (lane == 0) entry.adapter = a, entry.rows = n;
+    if ((uint32_t)at < (uint32_t)p.M) {  // (always, as long as the counter began at zero)
+      FewGroup& entry = p.groups[at];
+      if (lane < kRows) entry.row[lane] = mine;
+      if (lane == 0) entry.adapter = a, entry.rows = n;
+    }
   }
   if (a < 0) return;
   const int g = lane >> 2, t = lane & 3;
@@ -537,8 +539,11 @@ cudaError_t launch_adapter_few(AdapterFewParams p, int elem_in, int elem_out, in
   const int64_t groups = max_groups(p), resident = (int64_t)up_ctas_per_sm(rank_class(p.rank)) * sms;
   const int64_t shares =
       std::max<int64_t>(1, std::min<int64_t>((p.N + 32 * kWarps - 1) / (32 * kWarps), resident / groups));
-  return launch(f16 ? up_kernel<__half>(p.rank, elem_out) : up_kernel<__nv_bfloat16>(p.rank, elem_out),
-                dim3((unsigned)shares, (unsigned)groups, 1), p, stream);
+  const cudaError_t up = launch(f16 ? up_kernel<__half>(p.rank, elem_out) : up_kernel<__nv_bfloat16>(p.rank, elem_out),
+                                dim3((unsigned)shares, (unsigned)groups, 1), p, stream);
+  // (few_up leaves the counters at zero: without it, what few_down counted is cleared here)
+  if (up != cudaSuccess) cudaMemsetAsync(p.counts, 0, 2 * sizeof(uint32_t), stream);
+  return up;
 }
 
 }  // namespace gb300

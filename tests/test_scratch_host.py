@@ -105,3 +105,25 @@ def test_an_aborted_run_has_every_counter_cleared(fake):
     assert fake.lib.gemm_device_status(h, None, None) == 5
     assert _sizes(fake.journal(), "memset") == cleared
     fake.lib.gemm_destroy(h)
+
+
+def test_counters_are_zero_again_after_a_launch_that_fails(fake):
+    # (few_down has listed its groups, and few_up, which clears the list's length, never runs)
+    fake.journal()
+    h = fake.create()
+    try:
+        assert fake.run_adapters(h, 64, 512, 512, 16, 4, STREAM) == 0
+        journal = fake.journal()
+        counters = [p for w, p, n, *_ in journal if w == "memset" and n == 8]
+        assert len(counters) == 1
+        fake.lib.fake_fail(b"few_up_kernel")
+        assert fake.run_adapters(h, 64, 512, 512, 16, 4, STREAM) == 3  # GEMM_ERR_CUDA
+        after = fake.journal()
+        at = [w for w, *_ in after].index("failed-launch")
+        assert [(w, p, n, s) for w, p, n, s, _ in after[at + 1:]] == [("memset", counters[0], 8, STREAM)]
+        fake.lib.fake_fail(b"few_down_kernel")
+        assert fake.run_adapters(h, 64, 512, 512, 16, 4, STREAM) == 3
+    finally:
+        fake.lib.fake_fail(b"")
+    assert fake.run_adapters(h, 64, 512, 512, 16, 4, STREAM) == 0
+    fake.lib.gemm_destroy(h)
