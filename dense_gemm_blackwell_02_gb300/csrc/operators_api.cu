@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <utility>
 
 #include "context.h"
 #include "gemm.h"
@@ -69,6 +70,23 @@ bool takes_few_rows(const gemm_ctx* h, int64_t M, int64_t N, const gemm_adapters
   if (M > kFewRows) return M <= kFewRowsLargePool && ad->count > kLargePool;
   const bool wide = M > kAdapterRows && 4 * ceil_div(M, 256) * ceil_div(N, 256) > h->sms;
   return !(wide && nothing_forced(h) && ad->count <= 8 && ad->count * ad->rank <= 512);
+}
+
+// Whether two of n1 x n2 vectors of `dim` elements, s1 and s2 elements apart, share an element
+// (n1 and n2 at least 1).
+bool overlap(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t dim) {
+  if (n1 == 1) std::swap(n1, n2), std::swap(s1, s2);  // (of a single one the stride does not count)
+  if (n2 == 1) return n1 > 1 && s1 < dim;
+  if (s1 > s2) std::swap(n1, n2), std::swap(s1, s2);
+  if (s1 < dim) return true;
+  // j steps of s2 against the nearest numbers of steps of s1, as far as those reach
+  using wide = __int128;
+  const wide reach = (wide)(n1 - 1) * s1 + dim;
+  for (int64_t j = 1; j < n2 && (wide)j * s2 < reach; ++j) {
+    const wide at = (wide)j * s2, past = at % s1;
+    if (past < dim || (at / s1 + 1 < n1 && s1 - past < dim)) return true;
+  }
+  return false;
 }
 
 gemm_status_t launched(gemm_ctx* h, cudaError_t e) {
@@ -225,7 +243,9 @@ gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t token
       (r->inverse != 0 && r->inverse != 1))
     return GEMM_ERR_INVALID_ARG;
   if (!x || !y || !r->cos || !r->sin || !r->positions) return GEMM_ERR_INVALID_ARG;
-  if (x == y && (x_token_stride != y_token_stride || x_head_stride != y_head_stride))
+  // in place with other strides, where there are two tokens or heads for them to set apart
+  if (x == y && ((tokens > 1 && x_token_stride != y_token_stride) ||
+                 (heads > 1 && x_head_stride != y_head_stride)))
     return GEMM_ERR_INVALID_ARG;
   const int half = r->rot_dim / 2;
   if (r->pair_axis)
@@ -237,6 +257,8 @@ gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t token
   if (!aligned(x, (uint64_t)esz) || !aligned(y, (uint64_t)esz) || !aligned(r->cos, 4) ||
       !aligned(r->sin, 4) || !aligned(r->positions, 4))
     return GEMM_ERR_UNSUPPORTED;
+
+  if (overlap(tokens, y_token_stride, heads, y_head_stride, dim)) return GEMM_ERR_INVALID_ARG;
 
   RotaryParams p;
   std::memset(&p, 0, sizeof(p));

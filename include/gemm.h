@@ -477,8 +477,9 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
  *     a' = a cos - b sin,     b' = b cos + a sin
  *   x, y      tokens x heads x dim; element (t, h, d) of x at
  *             x + t * x_token_stride + h * x_head_stride + d elements, y likewise.  y may
- *             be x with the same strides (in place); otherwise they do not overlap.  The
- *             rotated heads may be the first of a fused projection's rows.
+ *             be x with the same strides (in place); otherwise they do not overlap.  Nor do
+ *             the heads of y one another.  The rotated heads may be the first of a fused
+ *             projection's rows.
  *   dtype     GEMM_F16, GEMM_BF16 or GEMM_F32, of x and y; computed in binary32 and
  *             rounded once
  *   rot_dim   even, 2..min(dim, 512): the first rot_dim values of a head are rot_dim / 2
@@ -508,8 +509,9 @@ typedef struct {
 
 /* Errors: GEMM_ERR_INVALID_ARG for a NULL handle, rotary or (with work to do) pointer,
  * negative sizes or strides, axes, rot_dim, pairs, inverse or a pair_axis out of range,
- * num_positions < 1, or y == x with other strides; GEMM_ERR_UNSUPPORTED for an FP8 dtype,
- * a pointer not aligned to its elements, or tokens * heads above INT32_MAX. */
+ * num_positions < 1, y == x with other strides, or strides of y that make its heads overlap;
+ * GEMM_ERR_UNSUPPORTED for an FP8 dtype, a pointer not aligned to its elements, or tokens *
+ * heads above INT32_MAX. */
 gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t tokens, int64_t heads,
                           int64_t dim, int64_t x_token_stride, int64_t x_head_stride,
                           int64_t y_token_stride, int64_t y_head_stride, gemm_dtype_t dtype,

@@ -51,3 +51,10 @@ class Fake:
         return self.lib.gemm_run_adapters_packed(_ADAPTERS_CALL.pack(
             h.value, 1 << 20, 2 << 20, 3 << 20, M, N, K, 4 << 20, stream, dtype, out, 5 << 20, 6 << 20,
             0, count, rank))
+
+    def rotary(self, h, tokens, heads, dim, x, y, pairs=4, in_place=False, dtype=1):
+        """x and y: (token stride, head stride) in elements."""
+        from dense_gemm_blackwell_02_gb300.binding import _ROTARY_CALL
+        return self.lib.gemm_rotary_packed(_ROTARY_CALL.pack(
+            h.value, 1 << 20, 1 << 20 if in_place else 2 << 20, tokens, heads, dim, *x, *y, 0, 3 << 20,
+            4 << 20, 5 << 20, 0, 100, 1, 2 * pairs, 0, 0, dtype, 0))
