@@ -46,6 +46,51 @@ __device__ __forceinline__ void load_row(const float* p, float (&f)[N]) {
   }
 }
 
+// A CTA's tokens and heads.
+struct Share {
+  int32_t t0, nt, h0, nh;
+  __device__ __forceinline__ explicit Share(const RotaryParams& p) {
+    const int32_t tile = (int32_t)(blockIdx.x / (uint32_t)p.shares);
+    const int32_t share = (int32_t)(blockIdx.x - (uint32_t)tile * (uint32_t)p.shares);
+    t0 = tile * p.tile_tokens, nt = min(p.tile_tokens, p.tokens - t0);
+    h0 = share * p.share_heads, nh = min(p.share_heads, p.heads - h0);
+  }
+};
+
+// The CTA's heads, pair by pair, for tokens with a position outside the tables: those pairs
+// stay as they are, infinities and NaN included, which a turn by no angle would not leave.
+template <typename T, bool NEIGH>
+__device__ __noinline__ void one_by_one(const RotaryParams& p, const float* table) {
+  const Share at(p);
+  const int t0 = at.t0, nt = at.nt, nh = at.nh;
+  const T* x = static_cast<const T*>(p.x) + (int64_t)t0 * p.x_token + (int64_t)at.h0 * p.x_head;
+  T* y = static_cast<T*>(p.y) + (int64_t)t0 * p.y_token + (int64_t)at.h0 * p.y_head;
+  const int per_head = p.half + (static_cast<const void*>(p.x) == p.y ? 0 : p.dim - 2 * p.half);
+  const int64_t all = (int64_t)nt * nh * per_head;
+  for (int64_t i = threadIdx.x; i < all; i += kThreads) {
+    const int64_t r = i / per_head;
+    const int e = (int)(i - r * per_head), t = (int)(r / nh), h = (int)(r - (int64_t)t * nh);
+    const T* from = x + t * p.x_token + h * p.x_head;
+    T* to = y + t * p.y_token + h * p.y_head;
+    if (e >= p.half) {  // past the pairs
+      to[e + p.half] = from[e + p.half];
+      continue;
+    }
+    const int ia = NEIGH ? 2 * e : e, ib = NEIGH ? 2 * e + 1 : e + p.half;
+    const T a = from[ia], b = from[ib];
+    const int64_t pos = p.positions[(int64_t)p.pair_axis[e] * p.tokens + t0 + t];
+    if (pos < 0 || pos >= p.num_positions) {
+      to[ia] = a;
+      to[ib] = b;
+      continue;
+    }
+    const float u = to_f32(a), v = to_f32(b);
+    const float c = table[t * 2 * p.half + e], s = table[t * 2 * p.half + p.half + e];
+    to[ia] = from_f32<T>(u * c - v * s);
+    to[ib] = from_f32<T>(v * c + u * s);
+  }
+}
+
 // NEIGH: neighbouring pairs.  V: elements per vector (1: no alignment is assumed).
 template <typename T, bool NEIGH, int V>
 __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
@@ -57,10 +102,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
   grid_dependency_wait();
   grid_launch_dependents();
 
-  const int32_t tile = (int32_t)(blockIdx.x / (uint32_t)p.shares);
-  const int32_t share = (int32_t)(blockIdx.x - (uint32_t)tile * (uint32_t)p.shares);
-  const int32_t t0 = tile * p.tile_tokens, nt = min(p.tile_tokens, p.tokens - t0);
-  const int32_t h0 = share * p.share_heads, nh = min(p.share_heads, p.heads - h0);
+  const Share at_share(p);
+  const int32_t t0 = at_share.t0, nt = at_share.nt, h0 = at_share.h0, nh = at_share.nh;
   const int lanes = min(p.items, kThreads);   // threads per head
   const int groups = kThreads / lanes;        // heads at a time
   const int g = (int)threadIdx.x / lanes;
@@ -167,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
   // (in place there is nothing to do past the pairs)
   const int items = static_cast<const void*>(p.x) == p.y ? pair_items : p.items;
   if (works && item < items) load(item, start);
+  int outside = 0;
   for (int i = (int)threadIdx.x; i < nt * p.half; i += kThreads) {
     const int t = i / p.half, pair = i - t * p.half;
     const int64_t pos = p.positions[(int64_t)p.pair_axis[pair] * p.tokens + t0 + t];
@@ -176,11 +220,15 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
       s = __ldg(p.sin + pos * p.half + pair);
     } else {
       record_bad_index(p.status, kSitePosition);
+      outside = 1;
     }
     table[t * 2 * p.half + pair] = c;
     table[t * 2 * p.half + p.half + pair] = p.inverse ? -s : s;
   }
-  __syncthreads();
+  if (__syncthreads_or(outside)) {
+    one_by_one<T, NEIGH>(p, table);
+    return;
+  }
   if (!works) return;
   for (; item < items; item += lanes) {
     Cursor c = start;

@@ -203,3 +203,38 @@ def test_empty_calls_and_refusals(g):
     with pytest.raises(KeyError):
         g.rotary(x.double(), x.double(), cos, sin, pos)
     assert g.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("D,half", [(64, 32), (70, 35), (80, 36)])
+def test_pairs_at_a_position_out_of_range_keep_infinities_and_nan(g, dt, neighbours, D, half):
+    # unturned means as they are: not a * 1 - b * 0, which is NaN for an infinite b.  Pairs of
+    # the other axis turn as always.
+    gen = torch.Generator().manual_seed(D)
+    x = torch.randn(9, 3, D, generator=gen).to(DT[dt])
+    inf = float("inf")
+    x[2, 1, 3], x[2, 2, 2 * half - 1], x[4, 0, 0], x[5, 1, half] = inf, -inf, float("nan"), inf
+    cos, sin = _tables(50, half)
+    pos = torch.tensor([[1, 49, 50, 3, -1, 2 ** 31 - 1, 0, 7, 8], [2, 3, 4, -7, 5, 6, 50, 7, 9]],
+                       dtype=torch.int32)
+    axes = [0] * (half // 2) + [1] * (half - half // 2)
+    out_of_range = (pos < 0) | (pos >= 50)
+    pair = torch.arange(half)
+    a, b = (2 * pair, 2 * pair + 1) if neighbours else (pair, pair + half)
+    axis = torch.zeros(D, dtype=torch.long)
+    axis[a] = axis[b] = torch.tensor(axes)
+    kept = out_of_range[axis].T[:, None, :].expand(9, 3, D).clone()
+    kept[..., 2 * half:] = True
+    y = torch.empty(9, 3, D, dtype=DT[dt], device="cuda")
+    g.rotary(x.cuda(), y, cos.cuda(), sin.cuda(), pos.cuda(), pair_axis=axes, neighbours=neighbours)
+    z = x.cuda()
+    g.rotary(z, z, cos.cuda(), sin.cuda(), pos.cuda(), pair_axis=axes, neighbours=neighbours)
+    assert g.device_status()[0] == 6
+    bits = torch.int32 if dt == "f32" else torch.int16
+    for got in (y.cpu(), z.cpu()):
+        assert torch.equal(got.view(bits)[kept], x.view(bits)[kept])
+        finite = torch.isfinite(x).all(dim=2)
+        want, mag = _expect(x[finite][:, None], cos, sin, pos[:, finite.nonzero()[:, 0]], axes,
+                            neighbours, False)
+        _check(got[finite][:, None], want, mag, dt)
