@@ -466,8 +466,8 @@ class Gemm:
         CUDA tensors logits and out (rows, vocab), rows of any stride, out possibly logits.
         tokens (int32) and token_start (int64, rows + 1) are the rows' histories, the first
         prompt_len (int32) of each the prompt; repetition, frequency and presence float32
-        (rows); bias_tokens (int32, ascending within a row), bias_values (float32) and
-        bias_start (int64, rows + 1) the biases; mask int32 (masks, words) with bit
+        (rows); bias_tokens (int32, fastest when ascending within a row), bias_values
+        (float32) and bias_start (int64, rows + 1) the biases; mask int32 (masks, words) with bit
         v % 32 of word v // 32 set where token v may follow, mask_row int32 (rows),
         negative for no mask, or None for one mask per row."""
         dev = logits.get_device()

@@ -61,8 +61,9 @@ struct RowRules {
   const uint32_t* mask;
 };
 
-// A token's logit through the penalties and biases its entry calls for.
-template <bool WIDE>
+// A token's logit through the penalties and biases its entry calls for.  ORDERED: the row's
+// biases are in the order of their tokens.
+template <bool WIDE, bool ORDERED>
 __device__ __forceinline__ float adjust(float z, uint32_t entry, int32_t v, const RowRules& r,
                                         const LogitsParams& p) {
   using E = Entry<WIDE>;
@@ -72,17 +73,96 @@ __device__ __forceinline__ float adjust(float z, uint32_t entry, int32_t v, cons
     if (c) z = z - r.freq * (float)c - r.pres;
   }
   if (entry & E::kHasBias) {
-    int64_t lo = r.bias0, hi = r.bias1;  // the first of the token's
-    while (lo < hi) {
-      const int64_t mid = lo + (hi - lo) / 2;
-      if (p.bias_tokens[mid] < v) lo = mid + 1;
-      else hi = mid;
-    }
     float w = 0.0f;
-    for (; lo < r.bias1 && p.bias_tokens[lo] == v; ++lo) w += p.bias_values[lo];
+    if constexpr (ORDERED) {
+      int64_t lo = r.bias0, hi = r.bias1;  // the first of the token's
+      while (lo < hi) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (p.bias_tokens[mid] < v) lo = mid + 1;
+        else hi = mid;
+      }
+      for (; lo < r.bias1 && p.bias_tokens[lo] == v; ++lo) w += p.bias_values[lo];
+    } else {
+      for (int64_t i = r.bias0; i < r.bias1; ++i)
+        if (p.bias_tokens[i] == v) w += p.bias_values[i];
+    }
     z += w;
   }
   return z;
+}
+
+// The logits of positions w0..w1-1 of a row (see do_slice) past the table; `next` holds the
+// thread's first whole vector.
+template <typename TI, typename TO, bool TABLE, bool WIDE, bool ORDERED>
+__device__ __forceinline__ void stream(const LogitsParams& p, const RowRules& r, const TI* in, TO* out,
+                                       int32_t shift, bool vec, int32_t w0, int32_t w1,
+                                       const uint32_t* table, Pack<TI, kVec> next) {
+  auto whole = [&](int32_t w) { return w >= shift && w - shift + kVec <= p.vocab; };
+  for (int32_t w = w0 + (int32_t)threadIdx.x * kVec; w < w1; w += kThreads * kVec) {
+    const int32_t v = w - shift;  // the first of kVec tokens; below 0 or past the end: none
+    float z[kVec];
+    if (vec && whole(w)) {
+      unpack(next, z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        z[j] = v + j >= 0 && v + j < p.vocab ? to_f32(in[v + j]) : 0.0f;
+    }
+    const int32_t ahead = w + kThreads * kVec;
+    if (vec && ahead < w1 && whole(ahead))
+      next = *reinterpret_cast<const Pack<TI, kVec>*>(in + ahead - shift);
+    if constexpr (TABLE) {
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const uint32_t entry = table[w - w0 + j];
+          if (entry) z[j] = adjust<WIDE, ORDERED>(z[j], entry, v + j, r, p);
+        }
+      } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(table + (w - w0) / 2);
+        if (a.x | a.y | a.z | a.w) {
+          const uint32_t two[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) {
+            const uint32_t entry = (two[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+            if (entry) z[j] = adjust<WIDE, ORDERED>(z[j], entry, v + j, r, p);
+          }
+        }
+      }
+    }
+    if (r.mask) {
+      // bit j: token v + j may follow
+      const int32_t last = (p.vocab - 1) >> 5;
+      const int32_t lo = v >> 5;  // (floor: -1 when v < 0)
+      const uint32_t word0 = lo >= 0 ? __ldg(r.mask + lo) : 0u;
+      const uint32_t word1 = lo < last && (v & 31) > 32 - kVec ? __ldg(r.mask + lo + 1) : 0u;
+      const uint32_t bits = __funnelshift_r(word0, word1, (uint32_t)(v & 31));
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (!((bits >> j) & 1u)) z[j] = __int_as_float(0xff800000);
+    }
+    if (vec && whole(w)) {
+      store_f32<TO, kVec>(out + v, z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (v + j >= 0 && v + j < p.vocab && w + j < w1) out[v + j] = from_f32<TO>(z[j]);
+    }
+  }
+}
+
+// The same for biases in any order: searched through from end to end.  Not inlined, so that it
+// takes nothing from the usual case (a flag that chose between the searches spilled there, and
+// a search behind a call took 97 us where 59 stayed).
+template <typename TI, typename TO, bool WIDE>
+__device__ __noinline__ void stream_unordered(const LogitsParams& p, RowRules r, const TI* in, TO* out,
+                                              int32_t shift, bool vec, int32_t w0, int32_t w1,
+                                              const uint32_t* table) {
+  Pack<TI, kVec> next;
+  const int32_t first = w0 + (int32_t)threadIdx.x * kVec;
+  if (vec && first < w1 && first >= shift && first - shift + kVec <= p.vocab)
+    next = *reinterpret_cast<const Pack<TI, kVec>*>(in + first - shift);
+  stream<TI, TO, true, WIDE, false>(p, r, in, out, shift, vec, w0, w1, table, next);
 }
 
 // Positions w0..w1-1 of a row (w0 a multiple of kVec; position w is token w - shift): the
@@ -117,64 +197,19 @@ __device__ __forceinline__ void do_slice(const LogitsParams& p, const RowRules& 
         else Entry<WIDE>::flag(table, at, Entry<WIDE>::kInPrompt);
       }
     }
+    int falls = 0;
     for (int64_t i = r.bias0 + threadIdx.x; i < r.bias1; i += kThreads) {
-      const uint32_t v = (uint32_t)__ldg(p.bias_tokens + i);
+      const int32_t token = __ldg(p.bias_tokens + i);
+      const uint32_t v = (uint32_t)token;
       if (v >= lo && v < hi) Entry<WIDE>::flag(table, (int32_t)v + shift - w0, Entry<WIDE>::kHasBias);
+      if (i > r.bias0 && __ldg(p.bias_tokens + i - 1) > token) falls = 1;
     }
-    __syncthreads();
-  }
-
-  for (int32_t w = first; w < w1; w += kThreads * kVec) {
-    const int32_t v = w - shift;  // the first of kVec tokens; below 0 or past the end: none
-    float z[kVec];
-    if (vec && whole(w)) {
-      unpack(next, z);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        z[j] = v + j >= 0 && v + j < p.vocab ? to_f32(in[v + j]) : 0.0f;
-    }
-    const int32_t ahead = w + kThreads * kVec;
-    if (vec && ahead < w1 && whole(ahead))
-      next = *reinterpret_cast<const Pack<TI, kVec>*>(in + ahead - shift);
-    if constexpr (TABLE) {
-      if constexpr (WIDE) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const uint32_t entry = table[w - w0 + j];
-          if (entry) z[j] = adjust<WIDE>(z[j], entry, v + j, r, p);
-        }
-      } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(table + (w - w0) / 2);
-        if (a.x | a.y | a.z | a.w) {
-          const uint32_t two[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            const uint32_t entry = (two[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-            if (entry) z[j] = adjust<WIDE>(z[j], entry, v + j, r, p);
-          }
-        }
-      }
-    }
-    if (r.mask) {
-      // bit j: token v + j may follow
-      const int32_t last = (p.vocab - 1) >> 5;
-      const int32_t lo = v >> 5;  // (floor: -1 when v < 0)
-      const uint32_t word0 = lo >= 0 ? __ldg(r.mask + lo) : 0u;
-      const uint32_t word1 = lo < last && (v & 31) > 32 - kVec ? __ldg(r.mask + lo + 1) : 0u;
-      const uint32_t bits = __funnelshift_r(word0, word1, (uint32_t)(v & 31));
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (!((bits >> j) & 1u)) z[j] = __int_as_float(0xff800000);
-    }
-    if (vec && whole(w)) {
-      store_f32<TO, kVec>(out + v, z);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (v + j >= 0 && v + j < p.vocab && w + j < w1) out[v + j] = from_f32<TO>(z[j]);
+    if (__syncthreads_or(falls)) {
+      stream_unordered<TI, TO, WIDE>(p, r, in, out, shift, vec, w0, w1, table);
+      return;
     }
   }
+  stream<TI, TO, TABLE, WIDE, true>(p, r, in, out, shift, vec, w0, w1, table, next);
 }
 
 // TABLE: there are histories or biases to look up.

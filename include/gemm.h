@@ -533,9 +533,10 @@ gemm_status_t gemm_rotary(gemm_handle_t h, const void* x, void* y, int64_t token
  *   repetition, frequency, presence
  *             one binary32 value per row; NULL: 1, 0 and 0
  *   bias_tokens, bias_values, bias_start
- *             row i's biases are entries bias_start[i] .. bias_start[i + 1] - 1, in the
- *             order of their tokens; several for one token add up, in that order.  Tokens
- *             outside 0..vocab - 1 are ignored.  bias_tokens NULL: no biases
+ *             row i's biases are entries bias_start[i] .. bias_start[i + 1] - 1, in any
+ *             order (fastest in that of their tokens); several for one token add up, in the
+ *             list's order.  Tokens outside 0..vocab - 1 are ignored.  bias_tokens NULL: no
+ *             biases
  *   mask, mask_stride, mask_count, mask_row
  *             mask_count bit masks of mask_stride 32-bit words (>= ceil(vocab / 32)); bit
  *             v % 32 of word v / 32 set: token v may follow.  Row i uses mask mask_row[i]

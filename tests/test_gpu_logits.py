@@ -255,3 +255,30 @@ def test_empty_calls_and_refusals(g):
     assert lib().gemm_adjust_logits(g.handle, x.data_ptr(), out.data_ptr(), 3, 100, 100, 100, 3, 2,
                                     ctypes.byref(a), None) == 2
     assert g.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("B,V,H,nb", [(4, 1000, 0, 50), (3, 30000, 64, 700), (5, 5000, 40000, 9)])
+def test_biases_in_any_order(g, dt, B, V, H, nb):
+    # rows in the order of their tokens beside rows in none, padding at the end of one, a fall
+    # at the last entry alone
+    t = _inputs(B, V, H, nb, 0, dt, seed=V + nb)
+    gen = torch.Generator().manual_seed(nb)
+    for i in range(B):
+        s0, s1 = t["bias_start"][i:i + 2].tolist()
+        if i % 3 == 0:
+            p = torch.randperm(s1 - s0, generator=gen)
+            t["bias_tokens"][s0:s1] = t["bias_tokens"][s0:s1][p]
+            t["bias_values"][s0:s1] = t["bias_values"][s0:s1][p]
+        elif i % 3 == 1 and s1 - s0 > 4:
+            t["bias_tokens"][s1 - 2:s1] = -1
+        elif s1 - s0 > 4:
+            t["bias_tokens"][s1 - 1] = t["bias_tokens"][s0]
+    out = torch.full(t["logits"].shape, 7.0, dtype=DT[dt], device="cuda")
+    d = {k: v.cuda() for k, v in t.items()}
+    g.adjust_logits(d.pop("logits"), out, **d)
+    # (the formula's index of the padding would be the last token's: a bias of 0 for the first)
+    padding = t["bias_tokens"] < 0
+    t["bias_values"][padding], t["bias_tokens"][padding] = 0.0, 0
+    _check(out, t, CODE[dt])
+    assert g.device_status()[0] == 0
