@@ -489,6 +489,9 @@ class Gemm:
             if mask.dim() != 2:
                 raise ValueError("mask must be (masks, words)")
             masks, words = mask.shape
+            # (an empty tensor has no address, which would say that there are no masks)
+            if masks * words == 0 and B and V:
+                raise ValueError("mask holds no mask")
         code = _lib.gemm_adjust_logits_packed(_LOGITS_CALL.pack(
             self._h.value or 0, logits.data_ptr(), out.data_ptr(), B, V, sl, so,
             _stream_of(stream, dev), _DTYPE_CODE[logits.dtype], _DTYPE_CODE[out.dtype],

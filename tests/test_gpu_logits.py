@@ -282,3 +282,16 @@ def test_biases_in_any_order(g, dt, B, V, H, nb):
     t["bias_values"][padding], t["bias_tokens"][padding] = 0.0, 0
     _check(out, t, CODE[dt])
     assert g.device_status()[0] == 0
+
+
+def test_an_empty_mask_is_refused_where_a_row_could_ask_for_it(g):
+    x = torch.zeros(2, 70, device="cuda")
+    rows = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for shape in ((0, 3), (2, 0)):
+        mask = torch.zeros(shape, dtype=torch.int32, device="cuda")
+        with pytest.raises(ValueError, match="mask"):
+            g.adjust_logits(x, torch.empty_like(x), mask=mask, mask_row=rows)
+        with pytest.raises(ValueError, match="mask"):
+            g.adjust_logits(x, torch.empty_like(x), mask=mask)
+    none = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+    g.adjust_logits(x[:0], torch.empty_like(x[:0]), mask=none, mask_row=rows[:0])
