@@ -236,7 +236,7 @@ template <typename T, int P>
 __global__ void __launch_bounds__(kThreads, 2)
     adapter_down_kernel(const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmDown, const AdapterParams p) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ TileSlots ts;
   __shared__ alignas(8) uint64_t bar_mem[kNumBars];
   __shared__ uint32_t tmem_slot;
