@@ -766,7 +766,8 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
   // (ADAPT: the preceding kernel is the one that prepares the adapters, itself started after
   // all work before it was complete; what the product reads and writes is not in its hands,
   // so the product starts beside its tail and each role waits where it first needs u or the
-  // tiles' lists.  The next kernel starts when this one's CTAs exit.)
+  // tiles' lists, and reads them past L1 and not as constant, since they are written while this
+  // kernel runs.  The next kernel starts when this one's CTAs exit.)
   if constexpr (!ADAPT) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -884,11 +885,11 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
           // the tile's adapters: u's parts, each with the adapter's rows of Up
           const AdapterTile* at = ad.tiles + w.m_blk;
           grid_dependency_wait();
-          const int32_t slots = w.kb1 == p.k_blocks ? __ldg(&at->slots) : 0;
+          const int32_t slots = w.kb1 == p.k_blocks ? __ldcg(&at->slots) : 0;
           const int32_t blocks = ad.rank <= kBlockK ? ad.parts : 2 * ad.parts;  // of u and of Up
           const CUtensorMap* mapUp = half ? &ad.tmUpHalf : &ad.tmUp;
           for (int32_t e = 0; ok && e < slots; ++e) {
-            const int32_t up_row = __ldg(&at->slot[e].adapter) * p.N + b_row;
+            const int32_t up_row = __ldcg(&at->slot[e].adapter) * p.N + b_row;
             for (int32_t x = 0; x < blocks; ++x) {
               if (!warp_wait_inl(empty_bar(stage), phase ^ 1u, ctl, kSiteEmpty)) {
                 ok = false;
@@ -1031,7 +1032,7 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
           if constexpr (ADAPT) {
             const AdapterTile* at = ad.tiles + w.m_blk;
             grid_dependency_wait();
-            const int32_t slots = ok && w.kb1 == p.k_blocks ? __ldg(&at->slots) : 0;
+            const int32_t slots = ok && w.kb1 == p.k_blocks ? __ldcg(&at->slots) : 0;
             if (slots > 0) {
               const uint32_t slot = iter & (kSlots - 1u), acc_phase = (iter >> kSlotShift) & 1u;
               if (!warp_wait_inl(acc_empty_bar(slot), acc_phase ^ 1u, ctl, kSiteAccEmpty)) break;
@@ -1039,8 +1040,8 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
               const uint32_t d_tmem = tmem_base + slot * BN;
               const int32_t blocks = ad.rank <= kBlockK ? ad.parts : 2 * ad.parts;
               for (int32_t e = 0; ok && e < slots; ++e) {
-                const uint4 off_lo = __ldg(reinterpret_cast<const uint4*>(at->slot[e].disable));
-                const uint4 off_hi = __ldg(reinterpret_cast<const uint4*>(at->slot[e].disable) + 1);
+                const uint4 off_lo = __ldcg(reinterpret_cast<const uint4*>(at->slot[e].disable));
+                const uint4 off_hi = __ldcg(reinterpret_cast<const uint4*>(at->slot[e].disable) + 1);
                 for (int32_t x = 0; x < blocks; ++x) {
                   if (!warp_wait_inl(full_bar(stage), phase, ctl, kSiteFull)) {
                     ok = false;
@@ -1261,9 +1262,9 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
       const int32_t my_m = w.m_blk * kRowsTile + (int32_t)rank * rows_cta + (int32_t)row;
       if constexpr (ADAPT) {
         grid_dependency_wait();
-        if (w.kb1 == p.k_blocks && __ldg(&ad.tiles[w.m_blk].slots) > 0) {
+        if (w.kb1 == p.k_blocks && __ldcg(&ad.tiles[w.m_blk].slots) > 0) {
           ++nchains;
-          if (my_m < p.M) row_factor = __ldg(ad.row_scale + my_m);
+          if (my_m < p.M) row_factor = __ldcg(ad.row_scale + my_m);
           if (row_factor < 0.0f) redo = (1u << kPieces) - 1u, row_factor = 0.0f;
         }
       }
