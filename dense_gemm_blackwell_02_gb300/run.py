@@ -52,8 +52,8 @@ def _moe_problems(name: str, experts: int, dev, gen):
 HIDDEN, HEADS_Q, HEADS_KV, HEAD_DIM = 8192, 64, 8, 128
 
 
-def serve(g: Gemm, rows: int, vocab: int, adapters: int, rank: int, reps: int, dev, gen) -> dict:
-    """`reps` decoding steps of `rows` requests; returns the last step's tokens."""
+def serve_state(rows: int, vocab: int, adapters: int, rank: int, dev, gen) -> dict:
+    """The model and the requests of serve()."""
     from .binding import pair_axes
 
     def normal(*shape, std=1.0):
@@ -64,35 +64,50 @@ def serve(g: Gemm, rows: int, vocab: int, adapters: int, rank: int, reps: int, d
     heads, half = HEADS_Q + HEADS_KV, HEAD_DIM // 2
     cols = (heads + HEADS_KV) * HEAD_DIM
     # the model: projections, a pool of adapters, the rotary tables
-    w_qkv, w_out = normal(cols, HIDDEN, std=HIDDEN ** -0.5), normal(vocab, HIDDEN, std=HIDDEN ** -0.5)
-    down, up = normal(adapters, rank, HIDDEN, std=HIDDEN ** -0.5), normal(adapters, cols, rank, std=0.02)
+    s = {"w_qkv": normal(cols, HIDDEN, std=HIDDEN ** -0.5),
+         "w_out": normal(vocab, HIDDEN, std=HIDDEN ** -0.5),
+         "down": normal(adapters, rank, HIDDEN, std=HIDDEN ** -0.5),
+         "up": normal(adapters, cols, rank, std=0.02)}
     angle = (torch.arange(4096, device=dev, dtype=torch.float64)[:, None]
              * 10000.0 ** (-torch.arange(half, device=dev, dtype=torch.float64) / half))
-    cos, sin = angle.cos().float(), angle.sin().float()
-    axes = pair_axes([half - 2 * (3 * half // 8), 3 * half // 8, 3 * half // 8])
+    s["cos"], s["sin"] = angle.cos().float(), angle.sin().float()
+    s["axes"] = pair_axes([half - 2 * (3 * half // 8), 3 * half // 8, 3 * half // 8])
     # the requests: their adapters (one in nine without), positions, histories, grammars
-    ids, positions = ints(-1, adapters, rows), ints(0, 4096, 3, rows)
+    s["ids"], s["positions"] = ints(-1, adapters, rows), ints(0, 4096, 3, rows)
     length = ints(1, 1025, rows).long()
     start = torch.cat([length.new_zeros(1), length.cumsum(0)])
     tokens = ints(0, vocab, int(start[-1]))
     ones = torch.ones(rows, device=dev)
     mask = ints(-2 ** 31, 2 ** 31 - 1, 2, (vocab + 31) // 32)
     mask_row = ints(-1, 2, rows)
-    x, hidden = normal(rows, HIDDEN), normal(rows, HIDDEN)
-    qkv = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
-    logits = torch.empty(rows, vocab, device=dev)
+    s["adjust"] = dict(tokens=tokens, token_start=start, prompt_len=(length // 2).int(),
+                       repetition=1.1 * ones, frequency=0.1 * ones, presence=0.1 * ones, mask=mask,
+                       mask_row=mask_row)
+    s["x"], s["hidden"] = normal(rows, HIDDEN), normal(rows, HIDDEN)
+    s["qkv"] = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+    s["logits"] = torch.empty(rows, vocab, device=dev)
+    return s
+
+
+def serve_step(g: Gemm, s: dict):
+    """One decoding step: fills s["qkv"] and s["logits"], returns the tokens."""
+    g.run_adapters(s["x"], s["w_qkv"], s["qkv"], s["down"], s["up"], s["ids"])
+    heads = HEADS_Q + HEADS_KV
+    qk = s["qkv"][:, :heads * HEAD_DIM].unflatten(1, (heads, HEAD_DIM))
+    g.rotary(qk, qk, s["cos"], s["sin"], s["positions"], pair_axis=s["axes"])
+    # (attention over qkv and the layers after it would give `hidden`)
+    g.run(s["hidden"], s["w_out"], s["logits"])
+    g.adjust_logits(s["logits"], s["logits"], **s["adjust"])
+    return s["logits"].argmax(dim=1)
+
+
+def serve(g: Gemm, rows: int, vocab: int, adapters: int, rank: int, reps: int, dev, gen) -> dict:
+    """`reps` decoding steps of `rows` requests; returns the last step's tokens."""
+    s = serve_state(rows, vocab, adapters, rank, dev, gen)
     for _ in range(reps):
-        g.run_adapters(x, w_qkv, qkv, down, up, ids)
-        qk = qkv[:, :heads * HEAD_DIM].unflatten(1, (heads, HEAD_DIM))
-        g.rotary(qk, qk, cos, sin, positions, pair_axis=axes)
-        # (attention over qkv and the layers after it would give `hidden`)
-        g.run(hidden, w_out, logits)
-        g.adjust_logits(logits, logits, tokens=tokens, token_start=start,
-                        prompt_len=(length // 2).int(), repetition=1.1 * ones,
-                        frequency=0.1 * ones, presence=0.1 * ones, mask=mask, mask_row=mask_row)
-        chosen = logits.argmax(dim=1)
+        chosen = serve_step(g, s)
     return {"serve": rows, "vocab": vocab, "adapters": adapters, "rank": rank,
-            "finite": bool(torch.isfinite(qkv).all()), "tokens": chosen[:8].tolist()}
+            "finite": bool(torch.isfinite(s["qkv"]).all()), "tokens": chosen[:8].tolist()}
 
 
 def main(argv=None) -> int:
