@@ -687,10 +687,16 @@ gemm_status_t run_impl(gemm_handle_t h, const void* A, const void* B, void* C, i
   const bool fp8_in = is_fp8(dtype_in);
   // A few rows of A: the CUDA-core matrix-vector path (variant 3), forced or automatic.
   // (Beside adapters a large matrix is faster in tiles, whose CTAs leave room for the other
-  // kernel: one adapter of rank 16, N x K, us: 8192 x 8192 31.6 against 33.2, 14336 x 4096
-  // 26.5 and 28.4, 14336 x 14336 71.7 and 78.5; 8192 x 2048 14.1 and 13.1.)
+  // kernel and which cut a long K: from 36 Mi weights on, or with a side of 10240.  One row, 8
+  // adapters of rank 16, N x K, us, tiles and matrix-vector: 5120 x 8192 24.3 and 26.1, 7168 x
+  // 8192 27.2 and 30.9, 8192 x 8192 29.8 and 32.8, 10240 x 4096 21.3 and 22.4; 10240 x 2048 14.0
+  // and 14.4, 28672 x 1024 17.6 and 19.0, 1024 x 14336 19.2 and 22.8; below, 1024 x 8192 16.6 and
+  // 15.0, 4096 x 8192 22.3 and 21.0, 7168 x 4096 18.0 and 17.7, 4096 x 4096 16.4 and 13.6, 2048 x
+  // 2048 11.3 and 7.6; where the line is off: 8192 x 4096 18.9 and 19.3, 10240 x 1024 10.7 and
+  // 10.5.)
   const gemm_config_t& fc = h->forced;
-  const bool tiles_beside = h->beside_rows && N >= 8192 && K >= 4096;
+  const bool tiles_beside =
+      h->beside_rows && (N * K >= (int64_t)36 << 20 || N >= 10240 || K >= 10240);
   if (fc.variant == 3 || (!fc.variant && !fc.block_n && !fc.splits && !fc.stages && !fc.epilogue &&
                           !fc.chain_kblocks && fc.swap_ab != 2 && M == 1 && K <= kGemvAutoMaxK && !tiles_beside &&
                           !fused && !fp8_in && !bs && !ad)) {
