@@ -437,6 +437,8 @@ gemm_status_t choose_plain(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out
 // finer slices add (16, 128 and 256 rows of A, binary32 results: N 1000 K 2048 8.0, 9.7 and
 // 10.1 us against 16.2, 19.3 and 20.8; N 1000 K 4096 9.6, 11.7 and 12.2 against 27.6, 30.9
 // and 33.2; N 2048 K 8192 16.2, 17.7 and 26.9 against 16.8, 18.6 and 28.7; equal at N 4096).
+// Not where such tiles leave no SMs for a second slice of a long K (256 x 5120 x 16384 with 16
+// adapters of rank 16: 67.8 us against 53.4).
 //
 // A grid that takes more than the product's share of the SMs, by the rows that either kernel
 // streams: the largest grid within that share, else the smallest that is a quarter of the
@@ -457,7 +459,8 @@ void choose_beside(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int kb
     return st == GEMM_OK;
   };
   const int64_t narrow = ceil_div(M, (int64_t)kBlockM) * ceil_div(N, (int64_t)128);
-  if (!c->kx2 && !c->sk_workers && c->dp_tiles == 0 && c->splits >= 3) {
+  if (!c->kx2 && !c->sk_workers && c->dp_tiles == 0 && c->splits >= 3 &&
+      (2 * narrow <= h->sms || c->k_blocks < 32)) {
     const int64_t s = std::min<int64_t>({h->sms / narrow, c->k_blocks / 16, 8});
     Choice to;
     if (forced(1, 128, (int)std::max<int64_t>(1, s), 0, &to)) *c = to;

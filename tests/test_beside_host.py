@@ -27,3 +27,13 @@ def _product(fake, M, N, K, rank=16, count=16):
 def test_one_row_takes_the_form_that_measured_faster(fake, N, K, tiles):
     name, _ = _product(fake, 1, N, K, count=8)
     assert ("gemv" not in name) == tiles, name
+
+
+def test_a_long_product_keeps_its_slices_where_narrow_tiles_could_have_none(fake):
+    # 80 tiles of 128 x 128 leave no SM for a second slice: K 16384 in one piece took 68 us, in
+    # the slices of wider tiles 53
+    assert _product(fake, 256, 5120, 16384)[1] >= 100
+    # where the tiles leave room, or K is short, they are taken
+    for M, N, K in ((16, 512, 8192), (64, 1024, 4096), (256, 1024, 4096), (256, 512, 1024)):
+        name, ctas = _product(fake, M, N, K)
+        assert "ILi1ELi128" in name, name
