@@ -381,21 +381,22 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
           for (int s = 0; s < P; ++s) mma_chunk<T>(acc[j], u0[s], u1[s], w[c][j]);
       }
     };
-    // Whether the warp's 32 columns have to be looked at again: the parts do not hold one of the
-    // rows, or there is an infinity or a NaN (times zero: NaN).  One vote; two, one for each
-    // half of the rows, cost the kernel 1 us in 10.
-    const bool wide = s0 < 0.0f || s1 < 0.0f;
-    auto look_again = [&](const float (&acc)[4][4]) {
+    // Whether a lane's columns of a row (first 0: row g, 2: row g + 8) hold an infinity or a NaN,
+    // which times zero is NaN; all four lanes' of the row where store() writes for all of them.
+    // (Votes in the loop make each step wait for its products: 1 us of the kernel's 10, 3 of 22
+    // with rank 64.)
+    auto left_out = [&](const float (&acc)[4][4], int first) {
       float z0 = 0.0f, z1 = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        fma2_rn(z0, z1, acc[j][0], acc[j][1], 0.0f);
-        fma2_rn(z0, z1, acc[j][2], acc[j][3], 0.0f);
-      }
-      return __any_sync(0xFFFFFFFFu, z0 + z1 != 0.0f || wide) != 0;
+      for (int j = 0; j < 4; ++j) fma2_rn(z0, z1, acc[j][first], acc[j][first + 1], 0.0f);
+      bool out = z0 + z1 != 0.0f;
+      if (!p.vec_store) out = ((__ballot_sync(0xFFFFFFFFu, out) >> (lane & ~3)) & 0xFu) != 0;
+      return out;
     };
-    bool again = false;
-    for (; q < groups; q += stride) {
+    // The parts do not hold one of the rows: all columns have to be looked at again.
+    const bool wide = __any_sync(0xFFFFFFFFu, s0 < 0.0f || s1 < 0.0f) != 0;
+    bool again = wide;
+    for (; !wide && q < groups; q += stride) {
       C bn[kChunks][4];
       float on[8];
       constexpr bool kAhead = RC <= 64;  // (128 values of a row twice do not fit the registers)
@@ -407,22 +408,22 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
       }
       float acc[4][4] = {};
       if (a >= 0) multiply(b, acc);
-      const bool skip = look_again(acc);
-      again |= skip;
+      const bool out0 = left_out(acc, 0), out1 = left_out(acc, 2);
+      again |= out0 || out1;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         o[2 * j] = fmaf(s0, acc[j][0], o[2 * j]);
         o[2 * j + 1] = fmaf(s0, acc[j][1], o[2 * j + 1]);
       }
-      if (!skip) store(q, row0, o);
-      if (live > 8 && !skip) {  // rows 8..15 of the group
+      store(q, out0 ? -1 : row0, o);
+      if (live > 8) {  // rows 8..15 of the group
         load_base(q, row1, o);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           o[2 * j] = fmaf(s1, acc[j][2], o[2 * j]);
           o[2 * j + 1] = fmaf(s1, acc[j][3], o[2 * j + 1]);
         }
-        store(q, row1, o);
+        store(q, out1 ? -1 : row1, o);
       }
       if (q + stride < groups) {
         if constexpr (kAhead) {
@@ -439,15 +440,15 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
       }
     }
     // The columns left out: rows that the parts do not hold, and what is not finite, in binary32.
-    if (again) {
+    if (__any_sync(0xFFFFFFFFu, again)) {
       for (q = (int)blockIdx.x * kWarps + warp; q < groups; q += stride) {
         load_up(q, b);
         float acc[4][4] = {};
         multiply(b, acc);
-        if (!look_again(acc)) continue;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int row = half ? row1 : row0;
+          const bool out = wide || left_out(acc, 2 * half);
+          const int row = !out ? -1 : half ? row1 : row0;
           const float s = half ? s1 : s0;
           load_base(q, row, o);
 #pragma unroll
