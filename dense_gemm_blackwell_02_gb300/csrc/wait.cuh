@@ -17,7 +17,10 @@ struct WaitCtl {
 
 __device__ __forceinline__ void record_timeout(const WaitCtl& c, uint32_t site) {
   *c.abort_flag = 1;
-  atomicCAS(c.status, 0u, (kDevTimeout << 24) | (site << 16) | (blockIdx.x & 0xFFFFu));
+  const uint32_t word = (kDevTimeout << 24) | (site << 16) | (blockIdx.x & 0xFFFFu);
+  // the first of several stays, but what is lost weighs more than an index not followed
+  const uint32_t before = atomicCAS(c.status, 0u, word);
+  if ((before >> 24) == kDevBadIndex) atomicCAS(c.status, before, word);
 }
 
 // Teardown wait: ignores the abort flag (it is used while aborting) but is bounded.

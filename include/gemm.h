@@ -357,7 +357,7 @@ gemm_status_t gemm_plan(const gemm_device_model_t* dev, const gemm_config_t* for
  * (the output of that run is undefined), GEMM_ERR_BAD_INDEX if a kernel of
  * gemm_run_adapters, gemm_rotary or gemm_adjust_logits met an index out of its
  * range (which it did not follow: see there), else GEMM_OK; of several only the
- * first.  *detail, if non-NULL, receives the raw word (code << 24 | site << 16 |
+ * first, but a wait given up before any index.  *detail, if non-NULL, receives the raw word (code << 24 | site << 16 |
  * block index). */
 gemm_status_t gemm_device_status(gemm_handle_t h, gemm_stream_t stream, uint32_t* detail);
 
