@@ -68,7 +68,8 @@ KERNEL_SOURCES = ("dense_gemm_blackwell_02_gb300/csrc/gemm_kernel.cuh",
                   "dense_gemm_blackwell_02_gb300/csrc/ptx.cuh",
                   "dense_gemm_blackwell_02_gb300/csrc/umma.cuh",
                   "dense_gemm_blackwell_02_gb300/csrc/params.h",
-                  "dense_gemm_blackwell_02_gb300/csrc/launch_impl.cuh")
+                  "dense_gemm_blackwell_02_gb300/csrc/launch_impl.cuh",
+                  "dense_gemm_blackwell_02_gb300/csrc/wait.cuh")
 
 
 def kernel_source_hash() -> str:

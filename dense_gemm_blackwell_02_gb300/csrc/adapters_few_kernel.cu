@@ -17,11 +17,12 @@
 // in order.  Ahead of the GEMM instead of beside it the whole is slower (64 adapters of
 // rank 16, 256 x 10240 x 8192 67 us against 55; 256 x 1000 x 2048 32 against 15).
 //
-// Measured, bf16 over cold operands, 256 x 10240 x 8192, 64 adapters of rank 16: 55 us, of
+// Measured, bf16 over cold operands, 256 x 10240 x 8192, 64 adapters of rank 16: 56 us, of
 // which the product alone is 40 (168 MB, 4.2 TB/s) and few_up after it 10 (Up's 21 MB from
 // HBM, the binary32 product's 10 MB from L2); few_down's 17 MB cost the product 5.  One row,
-// 8192 x 8192: 32 us, the product alone 26.  Looking further ahead in few_up spills and
-// costs 2 us; Up brought into L2 during the product gains nothing.
+// 8192 x 8192: 30 us, the product alone 26.  Binary32 results take a third part of u: 58 to 60
+// us for the first.  Looking further ahead in few_up spills and costs 2 us; Up brought into L2
+// during the product gains nothing.
 //
 // A dot product does not care in which order K is taken: lane t of a fragment's four reads
 // eight consecutive values, in both operands alike, where the fragment's layout would give

@@ -72,12 +72,6 @@ __device__ __forceinline__ Pack<T, N> pack(const float (&f)[N]) {
   return x;
 }
 
-// A plain (coherent) load: the operators may run in place.
-template <typename T, int N>
-__device__ __forceinline__ void load_f32(const T* p, float (&f)[N]) {
-  unpack(*reinterpret_cast<const Pack<T, N>*>(p), f);
-}
-
 template <typename T, int N>
 __device__ __forceinline__ void store_f32(T* p, const float (&f)[N]) {
   *reinterpret_cast<Pack<T, N>*>(p) = pack<T, N>(f);

@@ -443,10 +443,10 @@ gemm_status_t choose_plain(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out
 // A grid that takes more than the product's share of the SMs, by the rows that either kernel
 // streams: the largest grid within that share, else the smallest that is a quarter of the
 // SMs.  The other kernel has room for one CTA next to one of the product's, for six on an SM
-// of its own, and both are bound by how much they keep in flight (with 64 adapters of rank 64, 256 x 8192 x 8192: 64 CTAs 65 us against 88
-// for 128; 256 x 4096 x 4096 30 against 45; with 16 of rank 64, 256 x 8192 x 8192: 104 CTAs
-// 48 against 58; with 64 of rank 16, 256 x 10240 x 8192: 128 CTAs 54 against 62 for
-// stream-K on 152).
+// of its own, and both are bound by how much they keep in flight (with 64 adapters of rank 64,
+// 256 x 8192 x 8192: 64 CTAs 65 us against 88 for 128; 256 x 4096 x 4096 30 against 45; with 16
+// of rank 64, 256 x 8192 x 8192: 104 CTAs 48 against 58; with 64 of rank 16, 256 x 10240 x 8192:
+// 128 CTAs 54 against 62 for stream-K on 152).
 void choose_beside(gemm_ctx* h, int64_t M, int64_t N, int64_t K, int out, int kb_elems, Choice* c) {
   const gemm_config_t asked = h->forced;
   const auto forced = [&](int variant, int bn, int splits, int epilogue, Choice* to) {

@@ -624,11 +624,12 @@ static __device__ __noinline__ float adapter_term(const AdaptParams<true>& ad, i
 // ADAPT: low-rank adapters.  The last unit of every tile appends one chain in which each of
 // the tile's adapters multiplies the tile's rows of u (two or three 16-bit parts, from the
 // kernel before) by its rows of Up, into the accumulator rows that name it and no others
-// (`disable-output-lane`), so that a tile costs 2 rank / 64 K blocks more per adapter and Y
-// is rounded once; the epilogue scales that chain by the row's power of two.  8192 x 10240 x
-// 8192 with 12 adapters of rank 64 in runs of rows: 760 to 785 us with the kernel that
-// prepares u, where the product alone takes 780 at the same power cap; as a binary32 product
-// and a second pass over Y 1176 us.
+// (`disable-output-lane`), so that a tile costs 2 (3) rank / 64 K blocks more per adapter and Y
+// is rounded once; the epilogue multiplies that chain by the row's factor, and takes rows that
+// the parts do not hold, and what is not finite, in binary32 (RowFactor).  8192 x 10240 x 8192
+// with 12 adapters of rank 64 in runs of rows: 760 to 825 us with the kernel that prepares u,
+// where the product alone takes 780 at the same power cap; as a binary32 product and a second
+// pass over Y 1176 us.
 // CTA pairs, 256 columns, general epilogue.
 template <int CTA_GROUP, int BN, int STAGES, int OUT, bool ONE_CHAIN, bool FUSED, int KIND = 0,
           bool GROUPED = false, bool KX2 = false, bool STAGED = false, bool SWAP = false,

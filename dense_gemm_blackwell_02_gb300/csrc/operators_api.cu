@@ -1,7 +1,7 @@
 // C ABI of the operators around the projections (declared in include/gemm.h):
 // gemm_run_adapters, gemm_rotary and gemm_adjust_logits.  Argument validation,
-// workspace and launches; the kernels are in adapters_kernel.cu, rotary_kernel.cu and
-// logits_kernel.cu.
+// workspace and launches; the kernels are in adapters_few_kernel.cu, adapters_kernel.cu (and
+// gemm_kernel.cuh, ADAPT), rotary_kernel.cu and logits_kernel.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
