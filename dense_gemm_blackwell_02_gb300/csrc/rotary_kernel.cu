@@ -10,11 +10,12 @@
 // one vector of pairs of a head (two vectors of the head when a pair's halves lie apart, one
 // when they are neighbours) and walks the heads, several loads in flight.
 //
-// Measured over cold operands: 8192 tokens x 72 heads x 128, bf16, 53 us (302 MB at 5.7 TB/s,
-// 0.85 of a copy's rate); 4099 x 16 x 80 binary32, neighbours, 11.8 us (43 MB at 3.7 TB/s: a
-// second round of CTAs would be short, so the tokens per CTA are chosen for one); 256 x 72 x
-// 128 bf16 4.6 us and one token 2.2, both a launch and one trip to memory.  With the tables
-// read from L2 for every head and one head's loads in flight the first took 80 us.
+// Measured over cold operands: 8192 tokens x 72 heads x 128, bf16, 52 to 53 us (302 MB at 5.8
+// TB/s, 0.86 of a copy's rate); 4099 x 16 x 80 binary32, neighbours, 11.5 us (43 MB at 3.7 TB/s:
+// a second round of CTAs would be short, so the tokens per CTA are chosen for one); 256 x 72 x
+// 128 bf16 4.7 us and one token 2.3, both a launch and one trip to memory.  With the tables
+// read from L2 for every head and one head's loads in flight the first took 80 us.  Halves that
+// are no whole vectors move single elements: 8192 x 16 x 72 bf16 26.8 us, of 80 with 40 turned 43.
 #include <algorithm>
 
 #include "elements.cuh"
