@@ -223,11 +223,29 @@ __device__ __forceinline__ void ldg_chunk(uint2& v, const void* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
 }
 
+// The parts of neighbouring values of a row's second window: of those below `least`, divided by
+// the window's factor (0: the row has none).
+template <typename T, int P, typename C>
+__device__ __forceinline__ void low_parts(const float* u, float least, float factor, C (&part)[P]) {
+  constexpr int N = sizeof(C) / sizeof(T);
+  const float inv = factor != 0.0f ? 1.0f / factor : 0.0f;
+  Pack<T, N> to[P];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    T x[P];
+    split_f32(factor != 0.0f && fabsf(u[k]) < least ? u[k] * inv : 0.0f, x);
+#pragma unroll
+    for (int j = 0; j < P; ++j) to[j].v[k] = x[j];
+  }
+#pragma unroll
+  for (int j = 0; j < P; ++j) memcpy(&part[j], &to[j], sizeof(C));
+}
+
 __host__ __device__ constexpr int up_ctas_per_sm(int rc) { return rc <= 16 ? 6 : rc <= 32 ? 5 : 4; }
 
 // Grid: x a share of Y's columns, y the group.  RC: the rank's class, 16, 32, 64 or 128.  A
 // warp takes 32 columns at a time, and loads the next ones' weights and base before it
-// multiplies the present ones'.  u enters the MMA as 16-bit parts (row_factor, split_f32).
+// multiplies the present ones'.  u enters the MMA as 16-bit parts (RowFactor, split_f32).
 template <typename T, typename TO, int RC>
 __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
     few_up_kernel(const __grid_constant__ AdapterFewParams p) {
@@ -237,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
   constexpr int kPitch = RC + 8;  // values per row of a part: rows on different banks
   constexpr int P = u_parts(std::is_same<T, __nv_bfloat16>::value, std::is_same<TO, float>::value);
   __shared__ alignas(16) T part[P][kRows * kPitch];
-  __shared__ float row_scale[kRows];  // (RowFactor)
+  __shared__ float row_scale[kRows], row_scale_low[kRows];  // (RowFactor)
   __shared__ alignas(16) float u_mem[kRows][RC + 4];
   __shared__ float turn[kWarps][8][33];
   const int tid = (int)threadIdx.x, warp = (int)warp_id(), lane = (int)lane_id();
@@ -347,14 +365,14 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
         range.join(kLanes);
         const RowFactor to = row_factor<T>(range, std::is_same<TO, float>::value);
         if (i < kRows) {
-          if (c == 0) row_scale[i] = to.scale;
+          if (c == 0) row_scale[i] = to.scale, row_scale_low[i] = to.scale_low;
           store_f32<float, 8>(&u_mem[i][c], v);
           Pack<T, 8> x8[P];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             T x[P];
             // (a row with a NaN has NaN for its factor; its parts need not make more of them)
-            split_f32(isnan(to.scale) ? 0.0f : v[k] * to.inv, x);
+            split_f32(isnan(to.scale) ? 0.0f : to.high(v[k]), x);
 #pragma unroll
             for (int j = 0; j < P; ++j) x8[j].v[k] = x[j];
           }
@@ -394,8 +412,10 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
       if (!p.vec_store) out = ((__ballot_sync(0xFFFFFFFFu, out) >> (lane & ~3)) & 0xFu) != 0;
       return out;
     };
-    // The parts do not hold one of the rows: all columns have to be looked at again.
-    const bool wide = __any_sync(0xFFFFFFFFu, s0 < 0.0f || s1 < 0.0f) != 0;
+    // One of the rows has a second window, or is not held by its parts: its columns are all left
+    // to the second pass.
+    const float low0 = a >= 0 ? row_scale_low[g] : 0.0f, low1 = a >= 0 ? row_scale_low[g + 8] : 0.0f;
+    const bool wide = __any_sync(0xFFFFFFFFu, s0 < 0.0f || s1 < 0.0f || low0 != 0.0f || low1 != 0.0f) != 0;
     bool again = wide;
     for (; !wide && q < groups; q += stride) {
       C bn[kChunks][4];
@@ -440,26 +460,46 @@ __global__ void __launch_bounds__(kThreads, up_ctas_per_sm(RC))
         }
       }
     }
-    // The columns left out: rows that the parts do not hold, and what is not finite, in binary32.
+    // The columns left out: rows with a second window, those that the parts do not hold, and what
+    // is not finite, the last two in binary32.
     if (__any_sync(0xFFFFFFFFu, again)) {
+      const bool lows = __any_sync(0xFFFFFFFFu, low0 != 0.0f || low1 != 0.0f) != 0;
       for (q = (int)blockIdx.x * kWarps + warp; q < groups; q += stride) {
         load_up(q, b);
-        float acc[4][4] = {};
+        float acc[4][4] = {}, acc_low[4][4] = {};
         multiply(b, acc);
+        if constexpr (std::is_same<T, __half>::value) {
+          if (lows) {  // (the second window's parts: from u, at every step)
+            constexpr float kLeast = window_least(std::is_same<TO, float>::value);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const int k = (4 * c + t) * kValues;
+              C u0[P], u1[P];
+              low_parts<T, P>(&u_mem[g][k], kLeast * s0, low0, u0);
+              low_parts<T, P>(&u_mem[g + 8][k], kLeast * s1, low1, u1);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < P; ++s) mma_chunk<T>(acc_low[j], u0[s], u1[s], b[c][j]);
+            }
+          }
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const bool out = wide || left_out(acc, 2 * half);
           const int row = !out ? -1 : half ? row1 : row0;
-          const float s = half ? s1 : s0;
+          const float s = half ? s1 : s0, low = half ? low1 : low0;
           load_base(q, row, o);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float x = acc[k / 2][2 * half + k % 2];
             const int n = min(q * 32 + 8 * t + k, p.N - 1);
-            if (s < 0.0f || (s > 0.0f && !(fabsf(x) < __builtin_huge_valf())))
+            if (s < 0.0f || (s > 0.0f && !(fabsf(x) < __builtin_huge_valf()))) {
               o[k] += up_times_u(up + (int64_t)n * p.rank, u_mem[g + 8 * half], p.rank);
-            else
+            } else {
               o[k] = fmaf(s, x, o[k]);
+              if (low != 0.0f) o[k] = fmaf(low, acc_low[k / 2][2 * half + k % 2], o[k]);
+            }
           }
           store(q, row, o);
         }

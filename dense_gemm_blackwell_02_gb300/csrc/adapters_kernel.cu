@@ -19,8 +19,8 @@
 // u take the rest: the latency of its steps bounds it, not X's 17 MB.  Asking for X ahead of
 // the rows' adapters (into L2) delays the first K block by 2 us.
 //
-// u leaves as 16-bit parts, in fp16 times a power of two that brings the row into its range
-// (row_factor): one part alone would round u to 8 or 11 bits, an error of the size of Y's own
+// u leaves as 16-bit parts, in fp16 times a power of two that brings the row into its range,
+// with what is far below the row's largest in a second window (RowFactor): one part alone would round u to 8 or 11 bits, an error of the size of Y's own
 // rounding (how many, and what they leave: u_parts).  u itself goes along in binary32 for the
 // rows and columns that parts do not serve.
 #include <algorithm>
@@ -159,14 +159,14 @@ constexpr int kNumBars = 2 * kMaxStages + 3;
 constexpr uint32_t kRing = 96 * 1024;  // two CTAs per SM
 constexpr uint32_t kSmem = kRing + 1024;
 
-// N values times inv as P parts, kBlockK values apart.
-template <typename T, int N, int P>
-__device__ __forceinline__ void store_parts(T* to, const float (&v)[N], float inv) {
+// N values as P parts, kBlockK values apart; LOW: in the second window.
+template <typename T, int N, int P, bool LOW = false>
+__device__ __forceinline__ void store_parts(T* to, const float (&v)[N], const RowFactor& f) {
   struct alignas(N * sizeof(T)) { T x[N]; } part[P];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     T x[P];
-    split_f32(v[k] * inv, x);
+    split_f32(LOW ? f.low(v[k]) : f.high(v[k]), x);
 #pragma unroll
     for (int j = 0; j < P; ++j) part[j].x[k] = x[j];
   }
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ alignas(8) uint64_t bar_mem[kNumBars];
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t abort_mem;
+  __shared__ int32_t low_mem;  // a row that this CTA sees to has a second window
   const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const Bars bars{smem_addr(bar_mem)};
   const uint32_t warp = warp_id(), lane = lane_id();
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 0 && lane == 0) {
     bars.init();
     abort_mem = 0;
+    low_mem = 0;
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmDown);
   }
@@ -283,13 +285,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t n_max = ((uint32_t)(min(per_group, ts.slots) * p.rank) + 15u) & ~15u;
   const uint32_t stage_bytes = kTileBytes + n_max * kRowBytes;
   const uint32_t stages = min((uint32_t)kMaxStages, kRing / stage_bytes);
-  const int32_t pitch = P * kBlockK * (p.rank <= kBlockK ? 1 : 2);  // of U's rows
+  const int32_t window = P * kBlockK * (p.rank <= kBlockK ? 1 : 2);  // of U's rows
+  constexpr bool kWindows = std::is_same<T, __half>::value;
+  const int32_t pitch = (kWindows ? 2 : 1) * window;
   T* U = static_cast<T*>(p.U) + (int64_t)tile * kAdapterRows * pitch;
   // value c of a row: 64 at a time, their first parts before their second ones
   auto place_of = [](int32_t c) { return (c >> 6) * P * kBlockK + (c & (kBlockK - 1)); };
   if (cta == 0 && threadIdx.x < kAdapterRows && ts.slot[threadIdx.x] < 0 &&
-      tile * kAdapterRows + (int32_t)threadIdx.x < p.M)
+      tile * kAdapterRows + (int32_t)threadIdx.x < p.M) {
     p.row_scale[tile * kAdapterRows + (int32_t)threadIdx.x] = 0.0f;
+    p.row_scale_low[tile * kAdapterRows + (int32_t)threadIdx.x] = 0.0f;
+  }
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
@@ -383,7 +389,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int k = 0; k < 8; ++k) range.add(f * __uint_as_float(v[k]));
           }
           const RowFactor to = row_factor<T>(range, p.f32_out);
-          if (mine) p.row_scale[tile * kAdapterRows + row] = to.scale;
+          if (mine) {
+            p.row_scale[tile * kAdapterRows + row] = to.scale;
+            p.row_scale_low[tile * kAdapterRows + row] = to.scale_low;
+          }
+          bool low = false;
+          if constexpr (kWindows) {
+            low = __any_sync(0xFFFFFFFFu, mine && to.scale_low != 0.0f);
+            if (low) low_mem = 1;
+          }
           // (eight zeros past a rank that is not a multiple of the MMA's 16)
           for (int32_t c = 0; c < ((p.rank + 15) & ~15); c += 8) {
             uint32_t v[8] = {};
@@ -394,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             T* dst = U + (int64_t)row * pitch + place_of(c);
             if (mine && c < p.rank)
               store_f32<float, 8>(p.u + ((int64_t)tile * kAdapterRows + row) * p.rank + c, o);
-            if (mine) store_parts<T, 8, P>(dst, o, to.inv);
+            if (mine) store_parts<T, 8, P>(dst, o, to);
+            if (low && mine) store_parts<T, 8, P, true>(dst + window, o, to);
           }
         }
       }
@@ -448,17 +463,31 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         range.join(4);
         const RowFactor to = row_factor<T>(range, p.f32_out);
-        if (on && quad == 0) p.row_scale[tile * kAdapterRows + row] = to.scale;
+        if (on && quad == 0) {
+          p.row_scale[tile * kAdapterRows + row] = to.scale;
+          p.row_scale_low[tile * kAdapterRows + row] = to.scale_low;
+        }
+        const bool low = kWindows && on && to.scale_low != 0.0f;
+        if (low) low_mem = 1;
 #pragma unroll
         for (int q = 0; q < kQuads; ++q) {
           const int32_t c = (q * 4 + quad) * 4;
           T* dst = U + (int64_t)row * pitch + place_of(c);
-          if (on && c < ((p.rank + 15) & ~15)) store_parts<T, 4, P>(dst, v[q], to.inv);
+          if (on && c < ((p.rank + 15) & ~15)) store_parts<T, 4, P>(dst, v[q], to);
+        }
+        if (kWindows && __any_sync(0xFFFFFFFFu, low)) {  // (a branch: predicated it cost 3 us)
+#pragma unroll
+          for (int q = 0; q < kQuads; ++q) {
+            const int32_t c = (q * 4 + quad) * 4;
+            T* dst = U + (int64_t)row * pitch + window + place_of(c);
+            if (low && c < ((p.rank + 15) & ~15)) store_parts<T, 4, P, true>(dst, v[q], to);
+          }
         }
       }
     }
     cluster_sync();  // the others have read this CTA's sums
   }
+  if (kWindows && threadIdx.x == 0) p.low[tile * kAdaptCtas + cta] = (uint32_t)low_mem;
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, kAdapterCols);

@@ -109,19 +109,32 @@ struct RowRange {
   }
 };
 
-// The power of two that a row of u is multiplied by before it is split, and `scale`, which the
-// sum over the parts is multiplied by: the inverse; NaN for a row with a NaN; negative for a
-// row whose parts do not hold every value, to be multiplied in binary32 (up_times_u).
+// How a row of u goes into its 16-bit parts.  A value times `inv` is split; the sum over the
+// parts times `scale`, the inverse, is the row's term.  scale is NaN for a row with a NaN, and
+// negative for a row whose parts do not hold every value, to be multiplied in binary32.
 //
 // bf16 has binary32's range, short of the parts of values below 2^-100 (and of what rounds up
 // to an infinity).
 // fp16: the largest value comes to 2^14..2^15, and parts end at 2^-24, so that they leave up to
-// 2^-25 of a value.  Values below 2^-5 (2^-20 of the largest at most) would lose more than 2^-20
-// of themselves in a binary32 result, and values below 2^-8 more than 2^-17 in a 16-bit one.  Of
-// 64 normally distributed values one is that small in one row of 5000, and of 40000.
+// 2^-25 of a value.  What is then below `least`, 2^-5 (2^-20 of the largest at most), would lose
+// more than 2^-20 of itself in a binary32 result, and below 2^-8 more than 2^-17 in a 16-bit one.
+// Such values go into a second window: 2^(10 - log2 least) times themselves, below 2^15 again,
+// a sum of its own times `scale_low` (0: none of the row's values are there).  Two windows reach
+// 2^-39 (16-bit results: 2^-45) of the row's largest.  Of 64 normally distributed values one is in
+// the second window in one row of 5000 (40000), but a nearly dead rank has one in every row.
 struct RowFactor {
-  float inv = 1.0f, scale = 1.0f;
+  float inv = 1.0f, scale = 1.0f, least = 0.0f, inv_low = 0.0f, scale_low = 0.0f;
+  // A value of u in either window.
+  __device__ __forceinline__ float high(float u) const {
+    const float x = u * inv;
+    return fabsf(x) < least ? 0.0f : x;
+  }
+  __device__ __forceinline__ float low(float u) const {
+    return fabsf(u * inv) < least ? u * inv_low : 0.0f;
+  }
 };
+__host__ __device__ constexpr float window_least(bool f32_out) { return f32_out ? 0x1p-5f : 0x1p-8f; }
+__host__ __device__ constexpr float window_step(bool f32_out) { return 0x1p15f / window_least(f32_out); }
 template <typename T>
 __device__ __forceinline__ RowFactor row_factor(const RowRange& r, bool f32_out) {
   RowFactor f;
@@ -130,10 +143,18 @@ __device__ __forceinline__ RowFactor row_factor(const RowRange& r, bool f32_out)
     const int32_t e = min(max((int32_t)(r.most >> 23), 15), 254);
     f.inv = __uint_as_float((uint32_t)(268 - e) << 23);
     f.scale = __uint_as_float((uint32_t)(e - 14) << 23);
-    lowest = __float_as_uint((f32_out ? 0x1p-5f : 0x1p-8f) * f.scale);
+    f.least = window_least(f32_out);
+    const float first = f.least * f.scale, second = first / window_step(f32_out);
+    if (r.least < __float_as_uint(first) - 1u) {
+      f.inv_low = f.inv * window_step(f32_out);
+      f.scale_low = f.scale / window_step(f32_out);
+    }
+    lowest = max(__float_as_uint(second), 1u);
+    // (binary32 itself ends before the second window does)
+    if (isinf(f.inv_low) || (f.inv_low != 0.0f && f.scale_low < 0x1p-126f)) lowest = __float_as_uint(first);
   }
-  if (r.least < lowest - 1u || r.most > __float_as_uint(0x1.fep127f)) f.scale = -1.0f;
-  if (r.most > RowRange::kInf) f.scale = __int_as_float(0x7fc00000);
+  if (r.least < lowest - 1u || r.most > __float_as_uint(0x1.fep127f)) f.scale = -1.0f, f.scale_low = 0.0f;
+  if (r.most > RowRange::kInf) f.scale = __int_as_float(0x7fc00000), f.scale_low = 0.0f;
   return f;
 }
 

@@ -581,6 +581,15 @@ struct Layout {
                 "the A operand's 128-row span must stay inside the operand ring");
 };
 
+// (ADAPT) A lane's share of whether a row of the 256-row tile has a second window of u: any
+// lane's of a warp that is not zero says so.  (Asked for beside the tile's list, since each is a
+// trip to L2 that the tile's last MMAs wait for.)
+__device__ __forceinline__ uint32_t low_flag(const AdaptParams<true>& ad, int32_t m_blk) {
+  const int32_t t = 2 * m_blk + (int32_t)(lane_id() >> 3), c = (int32_t)(lane_id() & 7u);
+  const bool mine = ad.low != nullptr && lane_id() < 2 * kAdaptCtas && t < ad.low_tiles && c < ad.low_ctas;
+  return mine ? __ldcg(ad.low + t * kAdaptCtas + c) : 0u;
+}
+
 // (ADAPT, where the matrix instructions do not give it: see the epilogue) column n of row m's
 // adapter term.
 static __device__ __noinline__ float adapter_term(const AdaptParams<true>& ad, int32_t m, int32_t n, int32_t N) {
@@ -625,8 +634,10 @@ static __device__ __noinline__ float adapter_term(const AdaptParams<true>& ad, i
 // the tile's adapters multiplies the tile's rows of u (two or three 16-bit parts, from the
 // kernel before) by its rows of Up, into the accumulator rows that name it and no others
 // (`disable-output-lane`), so that a tile costs 2 (3) rank / 64 K blocks more per adapter and Y
-// is rounded once; the epilogue multiplies that chain by the row's factor, and takes rows that
-// the parts do not hold, and what is not finite, in binary32 (RowFactor).  8192 x 10240 x 8192
+// is rounded once; the epilogue multiplies that chain by the row's factor.  Where rows of the
+// tile have a second window of u, a second chain follows for it (fp16; 818 us against 842 with
+// such a value in every row); rows that neither holds, and what is not finite, are taken in
+// binary32 (RowFactor).  8192 x 10240 x 8192
 // with 12 adapters of rank 64 in runs of rows: 760 to 825 us with the kernel that prepares u,
 // where the product alone takes 780 at the same power cap; as a binary32 product and a second
 // pass over Y 1176 us.
@@ -886,10 +897,13 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
           // the tile's adapters: u's parts, each with the adapter's rows of Up
           const AdapterTile* at = ad.tiles + w.m_blk;
           grid_dependency_wait();
+          const uint32_t low = low_flag(ad, w.m_blk);
           const int32_t slots = w.kb1 == p.k_blocks ? __ldcg(&at->slots) : 0;
           const int32_t blocks = ad.rank <= kBlockK ? ad.parts : 2 * ad.parts;  // of u and of Up
           const CUtensorMap* mapUp = half ? &ad.tmUpHalf : &ad.tmUp;
-          for (int32_t e = 0; ok && e < slots; ++e) {
+          const int32_t windows = __any_sync(0xFFFFFFFFu, low != 0) ? 2 : 1;
+          for (int32_t i = 0; ok && i < windows * slots; ++i) {
+            const int32_t e = i < slots ? i : i - slots, x0 = i < slots ? 0 : blocks;
             const int32_t up_row = __ldcg(&at->slot[e].adapter) * p.N + b_row;
             for (int32_t x = 0; x < blocks; ++x) {
               if (!warp_wait_inl(empty_bar(stage), phase ^ 1u, ctl, kSiteEmpty)) {
@@ -900,7 +914,7 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
               if (leader) mbar_arrive_expect_tx_elect(full_bar(stage), tx);
               tma_load_2d_pair_elect(sB + stage * L::kBBytes, mapUp, x < ad.parts ? 0 : kBlockK, up_row,
                                      leader_full);
-              tma_load_2d_pair_elect(sA + stage * L::kABytes, &ad.tmU, x * kBlockK, a_row,
+              tma_load_2d_pair_elect(sA + stage * L::kABytes, &ad.tmU, (x0 + x) * kBlockK, a_row,
                                      leader_full);
               armed |= 1u << stage;
               armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
@@ -1033,10 +1047,15 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
           if constexpr (ADAPT) {
             const AdapterTile* at = ad.tiles + w.m_blk;
             grid_dependency_wait();
+            const uint32_t low = low_flag(ad, w.m_blk);
             const int32_t slots = ok && w.kb1 == p.k_blocks ? __ldcg(&at->slots) : 0;
-            if (slots > 0) {
+            const int32_t windows = slots == 0 ? 0 : __any_sync(0xFFFFFFFFu, low != 0) ? 2 : 1;
+            for (int32_t win = 0; ok && win < windows; ++win) {  // a chain for each
               const uint32_t slot = iter & (kSlots - 1u), acc_phase = (iter >> kSlotShift) & 1u;
-              if (!warp_wait_inl(acc_empty_bar(slot), acc_phase ^ 1u, ctl, kSiteAccEmpty)) break;
+              if (!warp_wait_inl(acc_empty_bar(slot), acc_phase ^ 1u, ctl, kSiteAccEmpty)) {
+                ok = false;
+                break;
+              }
               tc_fence_after();
               const uint32_t d_tmem = tmem_base + slot * BN;
               const int32_t blocks = ad.rank <= kBlockK ? ad.parts : 2 * ad.parts;
@@ -1258,14 +1277,20 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
       float acc[kHalf];
       const int32_t base_chains = chains_of(w, p.chain_kb);
       int32_t nchains = base_chains;
-      float row_factor = 0.0f;  // (ADAPT) of this thread's row in the adapters' chain
+      float row_factor = 0.0f;  // (ADAPT) of this thread's row in the adapters' chain,
+      float row_factor_low = 0.0f;  // and in the second window's
       uint32_t redo = 0;        // (ADAPT) bit pc: the row's adapter term there is not the MMAs'
       const int32_t my_m = w.m_blk * kRowsTile + (int32_t)rank * rows_cta + (int32_t)row;
       if constexpr (ADAPT) {
         grid_dependency_wait();
+        const uint32_t low = low_flag(ad, w.m_blk);
         if (w.kb1 == p.k_blocks && __ldcg(&ad.tiles[w.m_blk].slots) > 0) {
           ++nchains;
           if (my_m < p.M) row_factor = __ldcg(ad.row_scale + my_m);
+          if (__any_sync(0xFFFFFFFFu, low != 0)) {
+            ++nchains;
+            if (my_m < p.M) row_factor_low = __ldcg(ad.row_scale_low + my_m);
+          }
           if (row_factor < 0.0f) redo = (1u << kPieces) - 1u, row_factor = 0.0f;
         }
       }
@@ -1416,12 +1441,13 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
                   for (int j = 0; j < 32; ++j)
                     finite &= fabsf(__uint_as_float(r[j])) < __builtin_huge_valf() || n0 + j >= p.N;
                 }
-                if (!finite && row_factor > 0.0f) {
+                const float factor = ch == base_chains ? row_factor : row_factor_low;
+                if (!finite && factor > 0.0f && ch == base_chains) {
                   redo |= 1u << pc;
-                } else if (row_factor != 0.0f) {
+                } else if (factor != 0.0f && ((redo >> pc) & 1u) == 0) {
 #pragma unroll
                   for (int j = 0; j < 32; ++j)
-                    acc[32 * pc + j] = fmaf(row_factor, __uint_as_float(r[j]), acc[32 * pc + j]);
+                    acc[32 * pc + j] = fmaf(factor, __uint_as_float(r[j]), acc[32 * pc + j]);
                 }
               } else {
 #pragma unroll

@@ -120,8 +120,11 @@ struct AdapterParams {
   uint32_t idesc;       // instruction descriptor without N, 128 rows
   int32_t parts;        // of u (u_parts)
   int32_t f32_out;      // Y's type is binary32
-  void* U;              // M x (64 * parts * ceil(rank / 64)) values of the input type
+  void* U;              // M x (64 * parts * ceil(rank / 64)) values of the input type, twice that
+                        // in fp16, whose second half is the second window (RowFactor)
   float* row_scale;     // M (RowFactor)
+  float* row_scale_low; // M
+  uint32_t* low;        // kAdaptCtas per tile (AdaptParams)
   float* u;             // M x rank
   AdapterTile* pairs;   // ceil(tiles / 2)
   uint32_t* status;

@@ -192,18 +192,23 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
   p.test_stall = h->test_stall;
   p.f32_out = dtype_out == GEMM_F32;
   p.parts = u_parts(dtype_in == GEMM_BF16, dtype_out == GEMM_F32);
-  const int64_t pairs = ceil_div(p.tiles, 2), u_cols = p.parts * kBlockK * ceil_div(p.rank, kBlockK);
+  const bool windows = dtype_in == GEMM_F16;
+  const int64_t pairs = ceil_div(p.tiles, 2);
+  const int64_t u_cols = (windows ? 2 : 1) * p.parts * kBlockK * ceil_div(p.rank, kBlockK);
   const size_t u_bytes = round_up((size_t)M * u_cols * 2);
   const size_t scale_bytes = round_up((size_t)M * sizeof(float));
   const size_t pair_bytes = round_up((size_t)pairs * sizeof(AdapterTile));
+  const size_t low_bytes = windows ? round_up((size_t)p.tiles * kAdaptCtas * sizeof(uint32_t)) : 0;
   gemm_status_t st = ensure_scratch(
-      h, u_bytes + scale_bytes + pair_bytes + (size_t)M * p.rank * sizeof(float), 0);
+      h, u_bytes + 2 * scale_bytes + pair_bytes + low_bytes + (size_t)M * p.rank * sizeof(float), 0);
   if (st != GEMM_OK) return st;
   char* scratch = static_cast<char*>(h->op.ptr);
   p.U = scratch;
   p.row_scale = reinterpret_cast<float*>(scratch + u_bytes);
-  p.pairs = reinterpret_cast<AdapterTile*>(scratch + u_bytes + scale_bytes);
-  p.u = reinterpret_cast<float*>(scratch + u_bytes + scale_bytes + pair_bytes);
+  p.row_scale_low = reinterpret_cast<float*>(scratch + u_bytes + scale_bytes);
+  p.pairs = reinterpret_cast<AdapterTile*>(scratch + u_bytes + 2 * scale_bytes);
+  p.low = windows ? reinterpret_cast<uint32_t*>(scratch + u_bytes + 2 * scale_bytes + pair_bytes) : nullptr;
+  p.u = reinterpret_cast<float*>(scratch + u_bytes + 2 * scale_bytes + pair_bytes + low_bytes);
 
   CUtensorMap tmX, tmDown;
   AdaptParams<true> g;
@@ -215,6 +220,10 @@ gemm_status_t gemm_run_adapters(gemm_handle_t h, const void* X, const void* W, v
     return GEMM_ERR_CUDA;
   g.tiles = p.pairs;
   g.row_scale = p.row_scale;
+  g.row_scale_low = p.row_scale_low;
+  g.low = p.low;
+  g.low_tiles = p.tiles;
+  g.low_ctas = p.ctas;
   g.u = p.u;
   g.up = ad->up;
   g.row_adapter = row_adapter;

@@ -84,16 +84,23 @@ __host__ __device__ constexpr int u_parts(bool bf16_in, bool f32_out) {
   return bf16_in && f32_out ? 3 : 2;
 }
 
+constexpr int kAdaptCtas = 8;  // CTAs that share 128 rows in the kernel before, at most
+
 // What an ADAPT kernel takes beside GemmParams; nothing in the others.
 template <bool ADAPT>
 struct AdaptParams {};
 template <>
 struct AdaptParams<true> {
-  CUtensorMap tmU;        // u of every row, M x (64 * parts * ceil(rank / 64)): box {64, 128}
+  CUtensorMap tmU;        // u of every row, M x (64 * parts * ceil(rank / 64)), and as much again
+                          // for the second window where there can be one: box {64, 128}
   CUtensorMap tmUp;       // (adapters * N) x rank: box {64, BN / 2}
   CUtensorMap tmUpHalf;   // ... box {64, BN / 4} (half-tile units)
   const AdapterTile* tiles;
   const float* row_scale; // M: of each row's term (RowFactor), 0 without an adapter
+  const float* row_scale_low;  // M: of its second window
+  const uint32_t* low;    // kAdaptCtas per 128 rows: whether one of the rows that a CTA of the
+                          // kernel before saw to has a second window; nullptr: none can
+  int32_t low_tiles, low_ctas;
   const float* u;         // M x rank
   const void* up;
   const int32_t* row_adapter;

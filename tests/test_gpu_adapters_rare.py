@@ -130,3 +130,52 @@ def test_results_repeat(g, M, dout):
     for _ in range(5):
         again = _run(g, t, TD[dout])
         assert torch.equal(first.view(torch.uint8), again.view(torch.uint8))
+
+
+@pytest.mark.parametrize("M,N,K,R,L,din,dout,ids", [
+    (40, 320, 256, 16, 5, F16, F16, "mixed"),
+    (200, 1001, 520, 64, 7, F16, F32, "runs"),
+    (300, 264, 264, 128, 9, F16, BF16, "mixed"),
+    (1500, 1001, 136, 8, 70, F16, F32, "mixed"),
+    (700, 320, 256, 16, 5, F16, F16, "runs"),
+    (2560, 2304, 136, 72, 11, F16, F16, "runs"),
+    (600, 300, 8200, 16, 20, F16, F32, "mixed"),
+    (2600, 2653, 200, 16, 17, F16, F16, "runs"),
+])
+def test_rows_that_no_window_reaches_beside_rows_that_one_does(g, M, N, K, R, L, din, dout, ids):
+    # u's first value is 2^-28 of the others in some rows, 2^-48 in others, in some neither
+    t, rows = _case(M, N, K, R, L, din, ids, seed=M + R)
+    t["down"][:, 0, 0] = 2.0 ** -24
+    t["X"][:, 0] = 0
+    t["X"][rows, 0] = 2.0 ** -4
+    t["X"][rows[::2], 0] = 2.0 ** -24
+    t["X"][::3, 0] = 0
+    _check(_run(g, t, TD[dout]), t, dout)
+
+
+@pytest.mark.parametrize("M,ids", [(100, "mixed"), (2200, "runs")])
+@pytest.mark.parametrize("dout", [F16, F32])
+def test_an_adapter_with_a_nearly_dead_rank(g, M, ids, dout):
+    # every row has a value in the second window, and in each a column of Y that is that value's
+    # alone: the dead rank's own bits have to be there
+    gen = torch.Generator().manual_seed(M)
+    K, N, R, L = 256, 264, 16, 4
+    X = torch.randint(-8, 9, (M, K), generator=gen).half()
+    down = torch.randint(-8, 9, (L, R, K), generator=gen).half()
+    down[:, 5] = (torch.randint(-8, 9, (L, K), generator=gen) * 2.0 ** -20).half()
+    up = torch.zeros(L, N, R).half()
+    up[:, :, 5] = 64.0
+    up[:, 100:, 2] = 0.25
+    which = torch.randint(0, L, (M,), generator=gen, dtype=torch.int32)
+    which = which if ids == "mixed" else torch.sort(which).values
+    u = torch.stack([down[a].double() @ x.double() for a, x in zip(which.tolist(), X)])
+    want = torch.empty(M, N, dtype=torch.float64)
+    want[:, :100] = 64 * u[:, 5:6]
+    want[:, 100:] = 64 * u[:, 5:6] + u[:, 2:3] / 4
+    Y = torch.empty(M, N, dtype=torch.float16 if dout == F16 else torch.float32, device="cuda")
+    W = torch.zeros(N, K, dtype=torch.float16, device="cuda")
+    g.run_adapters(X.cuda(), W, Y, down.cuda(), up.cuda(), which.cuda())
+    torch.cuda.synchronize()
+    assert g.device_status() == (0, 0)
+    # integers (times 2^-20 for the dead rank) that both parts hold exactly
+    assert torch.equal(Y.cpu(), want.float().to(Y.dtype).cpu())
