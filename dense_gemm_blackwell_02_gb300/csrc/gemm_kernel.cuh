@@ -587,7 +587,7 @@ struct Layout {
 __device__ __forceinline__ uint32_t low_flag(const AdaptParams<true>& ad, int32_t m_blk) {
   const int32_t t = 2 * m_blk + (int32_t)(lane_id() >> 3), c = (int32_t)(lane_id() & 7u);
   const bool mine = ad.low != nullptr && lane_id() < 2 * kAdaptCtas && t < ad.low_tiles && c < ad.low_ctas;
-  return mine ? __ldcg(ad.low + t * kAdaptCtas + c) : 0u;
+  return mine ? ad.low[t * kAdaptCtas + c] : 0u;
 }
 
 // (ADAPT, where the matrix instructions do not give it: see the epilogue) column n of row m's
@@ -778,8 +778,8 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
   // (ADAPT: the preceding kernel is the one that prepares the adapters, itself started after
   // all work before it was complete; what the product reads and writes is not in its hands,
   // so the product starts beside its tail and each role waits where it first needs u or the
-  // tiles' lists, and reads them past L1 and not as constant, since they are written while this
-  // kernel runs.  The next kernel starts when this one's CTAs exit.)
+  // tiles' lists, and reads them by ordinary loads, not as constant, since they are written while
+  // this kernel runs.  The next kernel starts when this one's CTAs exit.)
   if constexpr (!ADAPT) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -898,13 +898,13 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
           const AdapterTile* at = ad.tiles + w.m_blk;
           grid_dependency_wait();
           const uint32_t low = low_flag(ad, w.m_blk);
-          const int32_t slots = w.kb1 == p.k_blocks ? __ldcg(&at->slots) : 0;
+          const int32_t slots = w.kb1 == p.k_blocks ? at->slots : 0;
           const int32_t blocks = ad.rank <= kBlockK ? ad.parts : 2 * ad.parts;  // of u and of Up
           const CUtensorMap* mapUp = half ? &ad.tmUpHalf : &ad.tmUp;
           const int32_t windows = __any_sync(0xFFFFFFFFu, low != 0) ? 2 : 1;
           for (int32_t i = 0; ok && i < windows * slots; ++i) {
             const int32_t e = i < slots ? i : i - slots, x0 = i < slots ? 0 : blocks;
-            const int32_t up_row = __ldcg(&at->slot[e].adapter) * p.N + b_row;
+            const int32_t up_row = at->slot[e].adapter * p.N + b_row;
             for (int32_t x = 0; x < blocks; ++x) {
               if (!warp_wait_inl(empty_bar(stage), phase ^ 1u, ctl, kSiteEmpty)) {
                 ok = false;
@@ -1048,7 +1048,7 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
             const AdapterTile* at = ad.tiles + w.m_blk;
             grid_dependency_wait();
             const uint32_t low = low_flag(ad, w.m_blk);
-            const int32_t slots = ok && w.kb1 == p.k_blocks ? __ldcg(&at->slots) : 0;
+            const int32_t slots = ok && w.kb1 == p.k_blocks ? at->slots : 0;
             const int32_t windows = slots == 0 ? 0 : __any_sync(0xFFFFFFFFu, low != 0) ? 2 : 1;
             for (int32_t win = 0; ok && win < windows; ++win) {  // a chain for each
               const uint32_t slot = iter & (kSlots - 1u), acc_phase = (iter >> kSlotShift) & 1u;
@@ -1060,8 +1060,8 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
               const uint32_t d_tmem = tmem_base + slot * BN;
               const int32_t blocks = ad.rank <= kBlockK ? ad.parts : 2 * ad.parts;
               for (int32_t e = 0; ok && e < slots; ++e) {
-                const uint4 off_lo = __ldcg(reinterpret_cast<const uint4*>(at->slot[e].disable));
-                const uint4 off_hi = __ldcg(reinterpret_cast<const uint4*>(at->slot[e].disable) + 1);
+                const uint4 off_lo = *reinterpret_cast<const uint4*>(at->slot[e].disable);
+                const uint4 off_hi = *(reinterpret_cast<const uint4*>(at->slot[e].disable) + 1);
                 for (int32_t x = 0; x < blocks; ++x) {
                   if (!warp_wait_inl(full_bar(stage), phase, ctl, kSiteFull)) {
                     ok = false;
@@ -1284,12 +1284,12 @@ __global__ void __launch_bounds__((Layout<CTA_GROUP, BN, STAGES, KX2, SWAP>::kTh
       if constexpr (ADAPT) {
         grid_dependency_wait();
         const uint32_t low = low_flag(ad, w.m_blk);
-        if (w.kb1 == p.k_blocks && __ldcg(&ad.tiles[w.m_blk].slots) > 0) {
+        if (w.kb1 == p.k_blocks && ad.tiles[w.m_blk].slots > 0) {
           ++nchains;
-          if (my_m < p.M) row_factor = __ldcg(ad.row_scale + my_m);
+          if (my_m < p.M) row_factor = ad.row_scale[my_m];
           if (__any_sync(0xFFFFFFFFu, low != 0)) {
             ++nchains;
-            if (my_m < p.M) row_factor_low = __ldcg(ad.row_scale_low + my_m);
+            if (my_m < p.M) row_factor_low = ad.row_scale_low[my_m];
           }
           if (row_factor < 0.0f) redo = (1u << kPieces) - 1u, row_factor = 0.0f;
         }
