@@ -14,7 +14,7 @@
 // Measured with the product: 8192 x 10240 x 8192, 12 adapters of rank 64 (prompts of some 700
 // rows, so that a tile multiplies by one or two), bf16, 760 to 825 us as the power cap has it,
 // 1690 to 1830 TFLOP/s (880 to 910 us when called back to back for seconds); 2050 x 4096 x 4096,
-// 6 of rank 32, fp16, 64 to 66 us, where the product alone takes 46 and rows without adapters 51.  Of the 15 us that this kernel has there, the first K block is in
+// 6 of rank 32, fp16, 65 to 66 us, where the product alone takes 46 and rows without adapters 51.  Of the 15 us that this kernel has there, the first K block is in
 // shared memory after 5.6, the MMAs are done after 9, and the clusters' sums and the stores of
 // u take the rest: the latency of its steps bounds it, not X's 17 MB.  Asking for X ahead of
 // the rows' adapters (into L2) delays the first K block by 2 us.
