@@ -10,10 +10,11 @@
 // The answer is a whole number that hangs on borders: 10^5 of them in a row without limits, so
 // that weights and sums good to 2^-24 would give another token than the formula in one row of a
 // hundred.  A weight is therefore a pair of binary32 values (Weight), good to 2^-34 of itself,
-// and sums are such pairs in a lane and whole numbers of 2^-42 across lanes: 64 bits hold 2^20
-// weights of 1, and the order of their additions does not matter.  (Binary64 has 1/64 of
-// binary32's rate on this GPU: sums over lanes in it took 25 us of one row's 30.)  Weights below
-// 2^-60 are 0.
+// and sums are such pairs in a lane and whole numbers across lanes, whose additions' order does not
+// matter: of 2^-42 in 64 bits, which hold 2^20 weights of 1, where short weights are enough, else of
+// 2^-62 in 128 bits.  (Binary64 has 1/64 of binary32's rate on this GPU: sums over lanes in it took 25
+// us of one row's 30.)  Weights below 2^-60 are 0; all others count: at the ends of u's range, which
+// no short weight decides, the answer may be any of them.
 //
 // One read of the logits: bound by HBM, if the passes over them stay on chip.  A row belongs to
 // a cluster of CTAs, each of which keeps its slice in shared memory, where it fits (else the later
@@ -97,15 +98,28 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // NaN is never chosen; -0 is 0.
 __device__ __forceinline__ float clean(float z) { return isnan(z) ? -__builtin_huge_valf() : z + 0.0f; }
 
-using Fixed = uint64_t;  // a sum of weights in units of 2^-kFixedBits
-constexpr int kFixedBits = 42;
+// Sums of weights as whole numbers.  Fixed: in units of 2^-kFixedBits, of all of a row's weights,
+// where a border that is not next to the sum decides; 2048 weights fit units of 2^-kListBits.  Whole:
+// in units of 2^-kWholeBits, in which no weight that counts (2^-60 and more) is 0, so that a sum above
+// 0 always has a token in it.
+using Fixed = uint64_t;
+constexpr int kFixedBits = 42, kListBits = 52, kWholeBits = 62;
+using Whole = unsigned __int128;
 
 // hi + lo, lo below half a step of hi.
 struct Weight {
   float hi, lo;
+  template <int BITS = kFixedBits>
   __device__ __forceinline__ Fixed fixed() const {
-    constexpr float kUnit = (float)(1ull << kFixedBits);
+    constexpr float kUnit = (float)(1ull << BITS);
     return (Fixed)(__float2ll_rn(hi * kUnit) + __float2ll_rn(lo * kUnit));
+  }
+  // (a weight is at most 1 ...
+  __device__ __forceinline__ Whole whole() const { return fixed<kWholeBits>(); }
+  // ... a sum of them, any number)
+  __device__ __forceinline__ Whole whole_sum() const {
+    const float of = floorf(hi);
+    return ((Whole)(uint64_t)of << kWholeBits) + (Whole)(__int128)(int64_t)Weight{hi - of, lo}.fixed<kWholeBits>();
   }
 };
 
@@ -115,6 +129,13 @@ __device__ __forceinline__ Fixed share_of(Fixed x, float share, bool up) {
   const uint64_t low = x * f;
   return (__umul64hi(x, f) << 1 | low >> 63) + (up && (low << 1) != 0 ? 1 : 0);
 }
+__device__ __forceinline__ Whole share_of(Whole x, float share, bool up) {
+  const uint64_t f = (uint64_t)__float2ll_rz(share * 9223372036854775808.0f);
+  const Whole high = (Whole)(uint64_t)(x >> 64) * f, low = (Whole)(uint64_t)x * f;  // (x below 2^83)
+  return (high << 1) + (low >> 63) + (up && (uint64_t)(low << 65 >> 64) != 0 ? 1 : 0);
+}
+// In the other units.
+__device__ __forceinline__ Fixed to_fixed(Whole x) { return (Fixed)(x >> (kWholeBits - kFixedBits)); }
 __device__ __forceinline__ float to_float(Fixed x) { return __ull2float_rn(x) * (1.0f / (float)(1ull << kFixedBits)); }
 
 struct Sum {
@@ -125,6 +146,7 @@ struct Sum {
     hi = s;
   }
   __device__ __forceinline__ Fixed value() const { return Weight{hi, lo}.fixed(); }
+  __device__ __forceinline__ Whole whole() const { return Weight{hi, lo}.whole_sum(); }
 };
 
 // A row's rules and a lane's way to the weights.
@@ -236,6 +258,8 @@ struct Shared {
   Fixed slots[2][kMaxCluster];      // a sum from every CTA of the cluster, in turn
   Fixed more_slots[kMaxCluster];
   Fixed parts[kWarps];
+  Whole whole_slots[2][kMaxCluster];
+  Whole whole_parts[kWarps];
   uint32_t count_parts[kWarps];
   float low_parts[kWarps], high_parts[kWarps];
   uint32_t ends[2];
@@ -329,24 +353,38 @@ __device__ __forceinline__ float largest(const Pack<T, 8>& x) {
 }
 
 // ----------------------------------------------------------------- sums over threads --
-// Of all threads, in every thread.
-__device__ __forceinline__ Fixed block_sum(Fixed s, Shared& sh) {
+template <typename S>
+__device__ __forceinline__ S from_lane_xor(S s, int off) { return __shfl_xor_sync(0xFFFFFFFFu, s, off); }
+__device__ __forceinline__ Whole from_lane_xor(Whole s, int off) {
+  return (Whole)__shfl_xor_sync(0xFFFFFFFFu, (uint64_t)(s >> 64), off) << 64 |
+         __shfl_xor_sync(0xFFFFFFFFu, (uint64_t)s, off);
+}
+template <typename S>
+__device__ __forceinline__ S from_lane_up(S s, int off) { return __shfl_up_sync(0xFFFFFFFFu, s, off); }
+__device__ __forceinline__ Whole from_lane_up(Whole s, int off) {
+  return (Whole)__shfl_up_sync(0xFFFFFFFFu, (uint64_t)(s >> 64), off) << 64 |
+         __shfl_up_sync(0xFFFFFFFFu, (uint64_t)s, off);
+}
+// Of all threads, in every thread, over parts[kWarps].
+template <typename S>
+__device__ __forceinline__ S block_sum(S s, S* parts) {
   const int warp = (int)warp_id();
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+  for (int off = 16; off > 0; off >>= 1) s += from_lane_xor(s, off);
   __syncthreads();
-  if (lane_id() == 0) sh.parts[warp] = s;
+  if (lane_id() == 0) parts[warp] = s;
   __syncthreads();
-  Fixed all = 0;
+  S all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += sh.parts[w];
+  for (int w = 0; w < kWarps; ++w) all += parts[w];
   return all;
 }
+__device__ __forceinline__ Fixed block_sum(Fixed s, Shared& sh) { return block_sum(s, sh.parts); }
 // Of the threads up to and with this one, over parts[kWarps].
 template <typename S>
 __device__ __forceinline__ S block_scan(S s, S* parts) {
   const int warp = (int)warp_id(), lane = (int)lane_id();
   for (int off = 1; off < 32; off <<= 1) {
-    const S o = __shfl_up_sync(0xFFFFFFFFu, s, off);
+    const S o = from_lane_up(s, off);
     if (lane >= off) s += o;
   }
   __syncthreads();
@@ -406,11 +444,13 @@ __device__ __forceinline__ float quotient(const Weight& w, Fixed whole) {
 }
 
 // The mass that top-p asks of a sum, rounded up, and the draw's share of it.
-__device__ __forceinline__ Fixed top_of(Fixed whole, float top_p) {
-  return top_p > 0.0f ? share_of(whole, top_p, true) : (Fixed)0;
+template <typename S>
+__device__ __forceinline__ S top_of(S whole, float top_p) {
+  return top_p > 0.0f ? share_of(whole, top_p, true) : (S)0;
 }
-__device__ __forceinline__ Fixed drawn_of(Fixed whole, float u) {  // (u of 1 and more: the last)
-  return u >= 1.0f ? whole : u > 0.0f ? share_of(whole, u, false) : (Fixed)0;
+template <typename S>
+__device__ __forceinline__ S drawn_of(S whole, float u) {  // (u of 1 and more: the last)
+  return u >= 1.0f ? whole : u > 0.0f ? share_of(whole, u, false) : (S)0;
 }
 
 // The first token, in the order of the index, at which the running sum of f exceeds goal_of(the
@@ -418,20 +458,20 @@ __device__ __forceinline__ Fixed drawn_of(Fixed whole, float u) {  // (u of 1 an
 // (token, f there, whole).  `lane_sum`: f's sum over this lane's share.
 template <typename T, typename G, typename F, typename D>
 __device__ __forceinline__ void locate_in(const Part<T>& part, Shared& sh, int turn, uint32_t ctas, uint32_t rank,
-                                          Fixed lane_sum, G goal_of, F f, D done) {
+                                          Whole lane_sum, G goal_of, F f, D done) {
   constexpr int V = Part<T>::V;
   const int tid = (int)threadIdx.x;
-  const Fixed mine = block_sum(lane_sum, sh);
-  if (tid < (int)ctas) *cluster_at(&sh.slots[turn][rank], (uint32_t)tid) = mine;
+  const Whole mine = block_sum(lane_sum, sh.whole_parts);
+  if (tid < (int)ctas) *cluster_at(&sh.whole_slots[turn][rank], (uint32_t)tid) = mine;
   cluster_barrier();
-  Fixed whole = 0;
-  for (uint32_t c = 0; c < ctas; ++c) whole += sh.slots[turn][c];
-  const Fixed goal = goal_of(whole);
+  Whole whole = 0;
+  for (uint32_t c = 0; c < ctas; ++c) whole += sh.whole_slots[turn][c];
+  const Whole goal = goal_of(whole);
   const bool past = goal >= whole;  // beyond all of it: the last token
-  Fixed before = 0, run = 0;
+  Whole before = 0, run = 0;
   int owner = 0;
   for (uint32_t c = 0; c < ctas; ++c) {
-    const Fixed of = sh.slots[turn][c];
+    const Whole of = sh.whole_slots[turn][c];
     if (of > 0 && (past || run <= goal)) owner = (int)c, before = run;
     run += of;
   }
@@ -440,7 +480,7 @@ __device__ __forceinline__ void locate_in(const Part<T>& part, Shared& sh, int t
   int w_at = 0;
   run = before;
   for (int w = 0; w < kWarps; ++w) {
-    const Fixed of = sh.parts[w];
+    const Whole of = sh.whole_parts[w];
     if (of > 0 && (past || run <= goal)) w_at = w, before = run;
     run += of;
   }
@@ -448,7 +488,7 @@ __device__ __forceinline__ void locate_in(const Part<T>& part, Shared& sh, int t
   const int32_t a = part.first_of(w_at), b = part.first_of(w_at + 1);
   const int32_t each_q = (b - a + kThreads - 1) / kThreads;
   const int32_t qa = a + tid * each_q, qb = min(qa + each_q, b);
-  Fixed own = 0;
+  Whole own = 0;
   auto walk = [&](auto g) {
     for (int32_t q = qa; q < qb; ++q) {
       float z[V];
@@ -457,9 +497,9 @@ __device__ __forceinline__ void locate_in(const Part<T>& part, Shared& sh, int t
       for (int j = 0; j < V; ++j) g(clean(z[j]), part.token(q) + j);
     }
   };
-  walk([&](float z, int32_t v) { own += f(z, v).fixed(); });
+  walk([&](float z, int32_t v) { own += f(z, v).whole(); });
   if (tid == 0) sh.found = -1;
-  run = before + block_scan(own, sh.parts) - own;  // (has the barriers)
+  run = before + block_scan(own, sh.whole_parts) - own;  // (has the barriers)
   // the last thread that begins at or below the goal and has something
   if (own > 0 && (past || run <= goal)) atomicMax(&sh.found, tid);
   __syncthreads();
@@ -468,7 +508,7 @@ __device__ __forceinline__ void locate_in(const Part<T>& part, Shared& sh, int t
     Weight wt{0.0f, 0.0f};
     walk([&](float z, int32_t v) {
       const Weight w = f(z, v);
-      const Fixed of = w.fixed();
+      const Whole of = w.whole();
       if (of > 0 && (past || run <= goal)) token = v, wt = w;
       run += of;
     });
@@ -520,6 +560,12 @@ struct Sum2 {
     parts_of(hi, a, b);
     parts_of(lo, c, d);
     return Weight{a, c}.fixed() + Weight{b, d}.fixed();
+  }
+  __device__ __forceinline__ Whole whole() const {
+    float a, b, c, d;
+    parts_of(hi, a, b);
+    parts_of(lo, c, d);
+    return Weight{a, c}.whole_sum() + Weight{b, d}.whole_sum();
   }
 };
 struct Pairs {
@@ -577,7 +623,7 @@ __device__ __noinline__ void exact_draw(const SampleParams& p, const Part<T>& pa
   constexpr int V = Part<T>::V;
   const int row = part.row;
   const Pairs pairs(st);
-  Fixed mine;
+  Whole mine;
   if (pairs.usable) {
     Sum2 sum;
     for (int32_t q = part.q0 + (int)lane_id(); q < part.q1; q += 32) {
@@ -599,19 +645,19 @@ __device__ __noinline__ void exact_draw(const SampleParams& p, const Part<T>& pa
         sum.add(w);
       }
     }
-    mine = sum.value();
+    mine = sum.whole();
   } else {
     Sum sum;
     part.each([&](float z, int32_t v) { sum.add(st.kept(z, v)); });
-    mine = sum.value();
+    mine = sum.whole();
   }
   const float u = p.random[row];
   locate_in<T>(part, sh, turn, (uint32_t)p.cluster, cluster_ctarank(), mine,
-               [&](Fixed whole) { return drawn_of(whole, u); },
+               [&](Whole whole) { return drawn_of(whole, u); },
                [&](float z, int32_t v) { return st.kept(z, v); },
-               [&](int32_t token, Weight w, Fixed whole) {
+               [&](int32_t token, Weight w, Whole whole) {
                  p.tokens[row] = token;
-                 if (p.probs) p.probs[row] = quotient(w, whole);
+                 if (p.probs) p.probs[row] = quotient(w, to_fixed(whole));
                });
 }
 
@@ -625,12 +671,12 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
   const float top_p = sh.rules.top_p;
   bool by_count = k >= 1 && k < p.vocab;
   const bool by_mass = top_p < 1.0f;
-  auto cluster_sum = [&](Fixed s) {  // of all CTAs' block sums, and a barrier of the cluster
-    const Fixed mine = block_sum(s, sh);
-    if (tid < (int)ctas) *cluster_at(&sh.slots[turn][rank], (uint32_t)tid) = mine;
+  auto cluster_sum = [&](Whole s) {  // of all CTAs' block sums, and a barrier of the cluster
+    const Whole mine = block_sum(s, sh.whole_parts);
+    if (tid < (int)ctas) *cluster_at(&sh.whole_slots[turn][rank], (uint32_t)tid) = mine;
     cluster_barrier();
-    Fixed all = 0;
-    for (uint32_t c = 0; c < ctas; ++c) all += sh.slots[turn][c];
+    Whole all = 0;
+    for (uint32_t c = 0; c < ctas; ++c) all += sh.whole_slots[turn][c];
     turn ^= 1;
     return all;
   };
@@ -638,14 +684,14 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
   auto locate = [&](auto goal_of, auto f, auto done) {
     Sum lane_sum;
     part.each([&](float z, int32_t v) { lane_sum.add(f(z, v)); });
-    locate_in<T>(part, sh, turn, ctas, rank, lane_sum.value(), goal_of, f, done);
+    locate_in<T>(part, sh, turn, ctas, rank, lane_sum.whole(), goal_of, f, done);
     turn ^= 1;
   };
 
   // Counts the tokens that stay so far, in the bracket's next bins; the cluster's first CTA
   // brackets the last token more closely: the one that makes the count reach `count_goal`, or, with
   // that 0, the mass reach `goal` (with `base` before the bracket).
-  auto narrow = [&](Bracket br, uint32_t count_goal, Fixed goal, Fixed base) {
+  auto narrow = [&](Bracket br, uint32_t count_goal, Whole goal, Whole base) {
     uint32_t* counts = region;
     uint32_t* sums = region + kBins;
     for (int i = tid; i < kBins; i += kThreads) counts[i] = 0;
@@ -694,7 +740,7 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
           if (run_c >= count_goal) atomicMin(&sh.found, tid * kMine + i);
         }
       } else {
-        const float goal_f = to_float(goal), base_f = to_float(base);
+        const float goal_f = to_float(to_fixed(goal)), base_f = to_float(to_fixed(base));
         float run_lo = base_f + (block_scan(lo, sh.low_parts) - lo), run_hi = base_f + (block_scan(hi, sh.high_parts) - hi);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
@@ -737,14 +783,14 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
       const float t = st.distance(z);
       if (t <= kMostLog2 && br.place(t) < 0 && st.inside(z, v)) s.add(st.weight(z));
     });
-    return cluster_sum(s.value());
+    return cluster_sum(s.whole());
   };
   auto mass_of_all = [&] {
     Sum s;
     part.each([&](float z, int32_t v) {
       if (st.inside(z, v)) s.add(st.weight(z));
     });
-    return cluster_sum(s.value());
+    return cluster_sum(s.whole());
   };
   // The second count's bins over the first one's bracket.
   auto finer = [&](Bracket br) {
@@ -796,18 +842,18 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
   auto listed_weight = [&](const uint64_t* list, int i) { return st.weight(key_value((uint32_t)(list[i] >> 32))); };
   // In the first CTA: the first place of list[0..count) at which the running mass reaches `goal`,
   // or (share) that part of the list's mass.
-  auto place_of_mass = [&](const uint64_t* list, int count, Fixed base, auto goal_of) {
+  auto place_of_mass = [&](const uint64_t* list, int count, Whole base, auto goal_of) {
     constexpr int kMine = kList / kThreads;
-    Fixed w[kMine], s = 0;
+    Whole w[kMine], s = 0;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int at = tid * kMine + i;
-      w[i] = at < count ? st.weight(key_value((uint32_t)(list[at] >> 32))).fixed() : 0;
+      w[i] = at < count ? st.weight(key_value((uint32_t)(list[at] >> 32))).whole() : 0;
       s += w[i];
     }
-    const Fixed goal = goal_of(block_sum(s, sh));
+    const Whole goal = goal_of(block_sum(s, sh.whole_parts));
     if (tid == 0) sh.found = count - 1;
-    Fixed run = base + (block_scan(s, sh.parts) - s);
+    Whole run = base + (block_scan(s, sh.whole_parts) - s);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       run += w[i];
@@ -816,7 +862,7 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
   };
   // Too many equal or nearly equal ones: the largest value of which the tokens at or above reach
   // the goal, by bisection, and then the index at which its equals do.
-  auto bisected = [&](bool count_goal, Fixed goal) {
+  auto bisected = [&](bool count_goal, Whole goal) {
     uint32_t lo = order_key(-3.402823466e38f), hi = order_key(st.m);
     auto above = [&](uint32_t key, bool equal) {
       const float edge = key_value(key);
@@ -827,7 +873,7 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
           if (w.hi > 0.0f) s.add(count_goal ? Weight{1.0f, 0.0f} : w);
         }
       });
-      return cluster_sum(s.value());
+      return cluster_sum(s.whole());
     };
     while (lo < hi) {
       const uint32_t mid = lo + (hi - lo) / 2 + 1;
@@ -835,14 +881,16 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
       else hi = mid - 1;
     }
     const float edge = key_value(lo);
-    const Fixed before = above(lo, false);
-    const Fixed one = count_goal ? (Fixed)1 << kFixedBits : max(st.weight(edge).fixed(), (Fixed)1);
-    const Fixed need = goal > before ? (goal - before + one - 1) / one : 1;
+    const Whole before = above(lo, false), lack = goal > before ? goal - before : 0;
+    const Whole one = count_goal ? (Whole)1 << kWholeBits : st.weight(edge).whole();
+    uint32_t need = 1;  // the fewest of the equals that reach the goal: (lack / one, rounded up)
+    for (uint32_t bit = (uint32_t)kMaxSampleVocab; bit > 0; bit /= 2)
+      if ((need + bit - 1) * one < lack) need += bit;
     // the need-th of the equals, or their last
     const RowState so_far = st;
-    locate([&](Fixed) { return (need << kFixedBits) - ((Fixed)1 << (kFixedBits - 1)); },
+    locate([&](Whole) { return ((Whole)need << kWholeBits) - ((Whole)1 << (kWholeBits - 1)); },
            [&](float z, int32_t v) { return Weight{z == edge && so_far.inside(z, v) ? 1.0f : 0.0f, 0.0f}; },
-           [&](int32_t token, Weight, Fixed) {
+           [&](int32_t token, Weight, Whole) {
              const Cut cut{edge, token};
              for (uint32_t cta = 0; cta < ctas; ++cta) *cluster_at(&sh.cut, cta) = cut;
            });
@@ -861,7 +909,7 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
       br.lo = 0, br.before = 0;
       sorted(br, [&](const uint64_t* list, int count) {
         const int kept = min(k, count);
-        if (by_mass) place_of_mass(list, kept, 0, [&](Fixed all) { return top_of(all, top_p); });
+        if (by_mass) place_of_mass(list, kept, 0, [&](Whole all) { return top_of(all, top_p); });
         else if (tid == 0) sh.found = kept - 1;
       });
       mass_done = true;
@@ -872,20 +920,20 @@ __device__ __noinline__ void exact_row(const SampleParams& p, const Part<T>& par
           if (tid == 0) sh.found = k - 1 - (int)br.before;
         });
       else
-        bisected(true, (Fixed)k << kFixedBits);
+        bisected(true, (Whole)k << kWholeBits);
     }
   }
   if (by_mass && !mass_done) {
-    const Fixed goal = top_of(mass_of_all(), top_p);
+    const Whole goal = top_of(mass_of_all(), top_p);
     Bracket br = narrow(Bracket::everything(), 0, goal, 0);
     if (br.count > kList) {
-      const Fixed base = mass_before(br);
+      const Whole base = mass_before(br);
       br = narrow(finer(br), 0, goal, base);
     }
     if (br.count <= kList) {
-      const Fixed base = mass_before(br);
+      const Whole base = mass_before(br);
       sorted(br, [&](const uint64_t* list, int count) {
-        place_of_mass(list, count, base, [&](Fixed) { return goal; });
+        place_of_mass(list, count, base, [&](Whole) { return goal; });
       });
     } else {
       bisected(false, goal);
@@ -1044,7 +1092,7 @@ __device__ __forceinline__ void short_list(const SampleParams& p, const RowState
     if (by_mass) {
 #pragma unroll
       for (int j = 0; j < kMine; ++j)
-        if (c.has(j)) sorted[rank[j]] = stays[j] ? w[j].fixed() : 0;
+        if (c.has(j)) sorted[rank[j]] = stays[j] ? w[j].fixed<kListBits>() : 0;
       __syncthreads();
       Fixed each_w[kMine], s = 0;
 #pragma unroll
@@ -1071,15 +1119,16 @@ __device__ __forceinline__ void short_list(const SampleParams& p, const RowState
       if (by_count) {
         last = cut_at(top_of(block_sum(s, sh), top_p));
       } else {
+        constexpr int kFiner = kListBits - kFixedBits;  // (the goal is at most the list's sum)
         const Fixed off = (whole >> 21) + (1 << 14);
-        last = cut_at(top_of(whole - off, top_p));
-        if (last != cut_at(top_of(whole + off, top_p))) {
+        last = cut_at(top_of(whole - off, top_p) << kFiner);
+        if (last != cut_at(top_of(whole + off, top_p) << kFiner)) {
           // the row's sum from whole weights, by this CTA alone
           const T* z = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
           Sum all;
 #pragma unroll 4
           for (int32_t v = tid; v < p.vocab; v += kThreads) all.add(st.weight(clean(to_f32(z[v]))));
-          last = cut_at(top_of(block_sum(all.value(), sh), top_p));
+          last = cut_at(top_of(block_sum(all.value(), sh), top_p) << kFiner);
         }
       }
 #pragma unroll
@@ -1097,7 +1146,7 @@ __device__ __forceinline__ void short_list(const SampleParams& p, const RowState
   c.ranks(sh, list, bins, [&](int j) { return c.token(j) >> down; }, [&](int j) { return (uint32_t)c.e[j]; }, rank);
 #pragma unroll
   for (int j = 0; j < kMine; ++j)
-    if (c.has(j)) sorted[rank[j]] = stays[j] ? w[j].fixed() : 0;
+    if (c.has(j)) sorted[rank[j]] = stays[j] ? w[j].fixed<kListBits>() : 0;
   __syncthreads();
   Fixed each_w[kMine], s = 0;
 #pragma unroll
@@ -1107,7 +1156,8 @@ __device__ __forceinline__ void short_list(const SampleParams& p, const RowState
   }
   if (tid == 0) sh.found = INT32_MAX, sh.found_lo = -1;
   const Fixed kept = block_sum(s, sh);
-  const Fixed goal = drawn_of(kept, p.random[row]);
+  const float u = p.random[row];
+  const Fixed goal = drawn_of(kept, u);
   Fixed run = block_scan(s, sh.parts) - s;
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
@@ -1117,13 +1167,19 @@ __device__ __forceinline__ void short_list(const SampleParams& p, const RowState
       atomicMax(&sh.found_lo, tid * kMine + j);
     }
   }
+  // at the ends of u's range the first and the last that stay, however small their weights
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    if (stays[j] && !(u > 0.0f)) atomicMin(&sh.found, rank[j]);
+    if (stays[j] && u >= 1.0f) atomicMax(&sh.found_lo, rank[j]);
+  }
   __syncthreads();
   const int at = sh.found != INT32_MAX ? sh.found : sh.found_lo;
 #pragma unroll
   for (int j = 0; j < kMine; ++j)
     if (c.has(j) && rank[j] == at) {
       p.tokens[row] = c.token(j);
-      if (p.probs) p.probs[row] = quotient(w[j], kept);
+      if (p.probs) p.probs[row] = quotient(w[j], kept >> (kListBits - kFixedBits));
     }
 }
 

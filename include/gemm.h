@@ -763,10 +763,11 @@ gemm_status_t gemm_norm_rotary_grad(gemm_handle_t h, const void* x, const void* 
  *                of those that stay, within 2^-20 of itself (1 where temperature is not above
  *                0)
  * NaN logits are never chosen, nor are logits of -infinity; a row that has nothing else
- * gets token -1 and probability 0.  Of logits of +infinity each has w = 1, all others 0.  A
- * w below 2^-60 counts as 0, and sums are whole numbers of 2^-42.  Where the result hangs on a
- * border between two tokens, weights good to 2^-34 decide, so that it is the formula's, and the
- * same from run to run.
+ * gets token -1 and probability 0.  Of logits of +infinity each has w = 1, all others 0, and so
+ * have logits further from m than binary32's largest number.  A w below 2^-60 counts as 0; every
+ * other one counts, also where random is 0 or 1.  Where the result hangs on a border between two
+ * tokens, weights good to 2^-34 decide, so that it is the formula's unless a running sum lies
+ * within 2^-33 of the whole from the border, and the same from run to run.
  * logits: rows x vocab with a row stride in elements; device memory, like all vectors (one
  * value per row), none of which may change while the call runs.  tokens and probs may not
  * overlap each other or an input.
