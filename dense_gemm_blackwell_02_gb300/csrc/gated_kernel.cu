@@ -64,10 +64,12 @@ __device__ __forceinline__ float2 gate_and_slope(float g) {
     const float cdf = 0.5f * erfcf(-0.70710678118654752f * g);
     return make_float2(g * cdf, fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), cdf));
   } else if constexpr (ACT == kGateGeluTanh) {
-    const float sq = fminf(g * g, 1e30f);  // (the slope's tail is 0, not 0 times infinity)
     const Logistic s = logistic(kTanhScale * g * fmaf(kTanhCube * g, g, 1.0f));
-    return make_float2(g * s.at, s.at * fmaf(kTanhScale * g * s.opposite,
-                                             fmaf(3.0f * kTanhCube, sq, 1.0f), 1.0f));
+    // (beyond 100 one side of the logistic function is 0: the slope is the other side then, and not
+    // 0 times an infinity)
+    const float near = fminf(fmaxf(g, -100.0f), 100.0f);
+    return make_float2(g * s.at, s.at * fmaf(kTanhScale * near * s.opposite,
+                                             fmaf(3.0f * kTanhCube, near * near, 1.0f), 1.0f));
   } else {
     return make_float2(g < 0.0f ? 0.0f : g, g > 0.0f ? 1.0f : 0.0f);
   }
