@@ -43,6 +43,56 @@ inline bool overlap(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t dim)
   return false;
 }
 
+// Memory of n1 x n2 vectors of `bytes` each, s1 and s2 bytes apart (none negative).
+struct Vectors {
+  using wide = __int128;
+  wide at, n1, s1, n2, s2, bytes;
+
+  // The same memory with the larger stride first, without strides that lead nowhere and with vectors
+  // that touch as one.
+  Vectors joined() const {
+    Vectors v = *this;
+    if (v.s1 == 0) v.n1 = 1;
+    if (v.s2 == 0) v.n2 = 1;
+    if (v.n1 == 1) v.s1 = 0;
+    if (v.n2 == 1) v.s2 = 0;
+    if (v.s1 < v.s2) std::swap(v.n1, v.n2), std::swap(v.s1, v.s2);
+    if (v.n2 > 1 && v.s2 <= v.bytes) v.bytes += (v.n2 - 1) * v.s2, v.n2 = 1, v.s2 = 0;
+    if (v.n2 == 1 && v.n1 > 1 && v.s1 <= v.bytes) v.bytes += (v.n1 - 1) * v.s1, v.n1 = 1, v.s1 = 0;
+    return v;
+  }
+  wide end() const { return at + (n1 - 1) * s1 + (n2 - 1) * s2 + bytes; }
+  // Whether p..p + len - 1 meets any of them.
+  bool meets(wide p, wide len) const {
+    const wide from = p - at - bytes, to = p - at + len;  // a vector that begins between the two does
+    if (to <= 0) return false;
+    const wide reach = from - (n2 - 1) * s2;
+    wide i = s1 == 0 || reach < 0 ? 0 : reach / s1 + 1;
+    for (; i < n1 && i * s1 < to; ++i) {
+      const wide rest = from - i * s1, j = rest < 0 ? 0 : s2 == 0 ? n2 : rest / s2 + 1;
+      if (j < n2 && i * s1 + j * s2 < to) return true;
+    }
+    return false;
+  }
+};
+
+// Whether a and b share a byte.
+inline bool share_memory(const Vectors& a_, const Vectors& b_) {
+  Vectors a = a_.joined(), b = b_.joined();
+  if (a.at >= b.end() || b.at >= a.end()) return false;
+  if (a.n1 == b.n1 && a.s1 == b.s1 && a.n2 == b.n2 && a.s2 == b.s2) {
+    // (of one layout only the vectors' distances count: those of b from a's first, either way)
+    b.at -= (a.n1 - 1) * a.s1 + (a.n2 - 1) * a.s2;
+    b.n1 = 2 * a.n1 - 1, b.n2 = 2 * a.n2 - 1;
+    return b.meets(a.at, a.bytes);
+  }
+  if (a.n1 * a.n2 > b.n1 * b.n2) std::swap(a, b);
+  for (Vectors::wide i = 0; i < a.n1; ++i)
+    for (Vectors::wide j = 0; j < a.n2; ++j)
+      if (b.meets(a.at + i * a.s1 + j * a.s2, a.bytes)) return true;
+  return false;
+}
+
 inline gemm_status_t launched(gemm_ctx* h, cudaError_t e) {
   h->last_cuda = e;
   if (e == cudaSuccess) return GEMM_OK;

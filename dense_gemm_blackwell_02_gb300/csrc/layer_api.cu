@@ -124,12 +124,31 @@ bool good_result(const Strides& s, int64_t tokens, int64_t heads, int64_t dim) {
   return !overlap(tokens, s.token, heads, s.head, dim);
 }
 
-// Elements per access (16 bytes' worth, 4 or 1) that all of the tensors allow: bases, strides, the
-// pairs' halves or ends and the heads' ends.
 struct Tensor {
   const void* p;
   Strides s;
 };
+
+Vectors memory_of(const Tensor& t, int64_t tokens, int64_t heads, int64_t dim, int dtype) {
+  const int64_t size = elem_size(dtype);
+  return {(Vectors::wide) reinterpret_cast<uintptr_t>(t.p), tokens, (Vectors::wide)t.s.token * size, heads,
+          (Vectors::wide)t.s.head * size, (Vectors::wide)dim * size};
+}
+// Whether `out` lies in the norms' weights, the tables or the positions.
+bool meets_tables(const Vectors& out, int64_t tokens, int64_t dim, const gemm_head_norm_t* n, const gemm_rotary_t* r) {
+  const Vectors::wide table = (Vectors::wide)r->num_positions * (r->rot_dim / 2) * 4, w = dim * elem_size(n->weight_dtype);
+  const struct {
+    const void* p;
+    Vectors::wide bytes;
+  } all[] = {{r->cos, table}, {r->sin, table}, {r->positions, (Vectors::wide)r->axes * tokens * 4},
+             {n->query_weight, w}, {n->key_weight, w}};
+  for (const auto& t : all)
+    if (t.p && share_memory(out, {(Vectors::wide) reinterpret_cast<uintptr_t>(t.p), 1, 0, 1, 0, t.bytes})) return true;
+  return false;
+}
+
+// Elements per access (16 bytes' worth, 4 or 1) that all of the tensors allow: bases, strides, the
+// pairs' halves or ends and the heads' ends.
 int heads_vector(std::initializer_list<Tensor> tensors, int64_t tokens, int64_t heads, int64_t dim,
                  int dtype, const gemm_rotary_t* r) {
   const int64_t pairs = r->pairs == GEMM_PAIRS_NEIGHBOURS ? r->rot_dim : r->rot_dim / 2;
@@ -369,6 +388,8 @@ gemm_status_t gemm_norm_rotary(gemm_handle_t h, const void* x, void* y, int64_t 
   if (st != GEMM_OK || !work) return st;
   if (!x || !y || (x == y && differ(sx, sy, tokens, heads))) return GEMM_ERR_INVALID_ARG;
   if (!good_result(sy, tokens, heads, dim)) return GEMM_ERR_INVALID_ARG;
+  const Vectors mx = memory_of({x, sx}, tokens, heads, dim, dtype), my = memory_of({y, sy}, tokens, heads, dim, dtype);
+  if ((x != y && share_memory(my, mx)) || meets_tables(my, tokens, dim, norm, r)) return GEMM_ERR_INVALID_ARG;
   if (!aligned(x, (uint64_t)elem_size(dtype)) || !aligned(y, (uint64_t)elem_size(dtype)))
     return GEMM_ERR_UNSUPPORTED;
   HeadsParams p = heads_params(h, tokens, heads, dim, norm, r);
@@ -398,6 +419,7 @@ gemm_status_t gemm_norm_rotary_grad(gemm_handle_t h, const void* x, const void* 
   bool work;
   gemm_status_t st = check_heads(tokens, heads, dim, dtype, norm, r, &work);
   if (st != GEMM_OK) return st;
+  if (meet({d_query_weight, 4 * dim}, {d_key_weight, 4 * dim})) return GEMM_ERR_INVALID_ARG;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (!work) {  // sums of nothing
     for (float* w : {d_query_weight, d_key_weight})
@@ -407,6 +429,15 @@ gemm_status_t gemm_norm_rotary_grad(gemm_handle_t h, const void* x, const void* 
   }
   if (!x || !dy || !dx || (dy == dx && differ(sg, sd, tokens, heads)) || x == dx) return GEMM_ERR_INVALID_ARG;
   if (!good_result(sd, tokens, heads, dim)) return GEMM_ERR_INVALID_ARG;
+  const Vectors mx = memory_of({x, sx}, tokens, heads, dim, dtype), mg = memory_of({dy, sg}, tokens, heads, dim, dtype),
+                md = memory_of({dx, sd}, tokens, heads, dim, dtype);
+  if (share_memory(md, mx) || (dy != dx && share_memory(md, mg)) || meets_tables(md, tokens, dim, norm, r))
+    return GEMM_ERR_INVALID_ARG;
+  for (const float* w : {d_query_weight, d_key_weight}) {
+    const Vectors m = {(Vectors::wide) reinterpret_cast<uintptr_t>(w), 1, 0, 1, 0, (Vectors::wide)dim * 4};
+    if (w && (share_memory(m, mx) || share_memory(m, mg) || share_memory(m, md) || meets_tables(m, tokens, dim, norm, r)))
+      return GEMM_ERR_INVALID_ARG;
+  }
   for (const void* q : {x, dy, static_cast<const void*>(dx)})
     if (!aligned(q, (uint64_t)elem_size(dtype))) return GEMM_ERR_UNSUPPORTED;
   HeadsParams p = heads_params(h, tokens, heads, dim, norm, r);

@@ -704,6 +704,7 @@ gemm_status_t gemm_run_gated_grad(gemm_handle_t h, const void* X, const void* ga
  *   query_weight, key_weight  dim values of weight_dtype (GEMM_F16, GEMM_BF16 or GEMM_F32) in
  *                device memory; NULL: all 1
  *   eps          >= 0; the squares are summed in binary32
+ * y shares no memory with the weights, the tables or the positions, nor with x unless it is x.
  */
 typedef struct {
   const void* query_weight;
@@ -714,7 +715,8 @@ typedef struct {
 } gemm_head_norm_t;
 
 /* Errors as gemm_rotary, and: GEMM_ERR_INVALID_ARG for a NULL norm, query_heads out of
- * range, a negative eps, an unknown weight_dtype, or rotary->inverse not 0;
+ * range, a negative eps, an unknown weight_dtype, rotary->inverse not 0, or a y that overlaps
+ * an input otherwise than in place;
  * GEMM_ERR_UNSUPPORTED for dim above 512, FP8 weights, or weights not aligned to their
  * elements. */
 gemm_status_t gemm_norm_rotary(gemm_handle_t h, const void* x, void* y, int64_t tokens,
@@ -729,11 +731,13 @@ gemm_status_t gemm_norm_rotary(gemm_handle_t h, const void* x, void* y, int64_t 
  * dn = R^T dy and g = w * dn
  *     dx = r g - x r^3 mean(g * x),      dw = sum over tokens and heads of dn * x * r
  *   dx                            like y; it may be dy with the same strides (in place), but
- *                                 not x
+ *                                 shares no memory with x, nor otherwise with dy
  *   d_query_weight, d_key_weight  dim binary32 values each, overwritten: the sums over the
  *                                 first query_heads heads and over the others (zeros where
- *                                 there are none); each may be NULL
- * The same bits from run to run. */
+ *                                 there are none); each may be NULL.  They share no memory
+ *                                 with each other, with dx or with an input
+ * The same bits from run to run.  Errors as gemm_norm_rotary, and GEMM_ERR_INVALID_ARG for
+ * results that overlap as above. */
 gemm_status_t gemm_norm_rotary_grad(gemm_handle_t h, const void* x, const void* dy, void* dx,
                                     int64_t tokens, int64_t heads, int64_t dim,
                                     int64_t x_token_stride, int64_t x_head_stride,
