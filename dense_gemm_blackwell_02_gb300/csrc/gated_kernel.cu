@@ -4,8 +4,9 @@
 //     dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X
 // X: M x K, Wg and Wu: N x K, H: M x N.  Sums in binary32 (Tensor Memory), rounded once to the
 // outputs' type; dG and dU are rounded to the element type between the two steps of the backward
-// pass, because the matrix instructions take 16-bit operands: half a step of each term of a long
-// sum, less than the rounding of the result itself adds.
+// pass, because the matrix instructions take 16-bit operands: half a step of each term, which over a
+// long sum adds about as much error as the rounding of the result itself, and more where its terms
+// cancel.  In fp16 their range is widened by scales of rows and columns (GatedRange).
 //
 // Many rows: a CTA pair computes a 256 x 256 accumulator (cta_group::2).  In the forward pass its
 // columns are 128 of G and the same 128 of U: the leader loads rows of Wg, its peer rows of Wu, so
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(PairLayout::kThreads, 1)
   using L = PairLayout;
   constexpr int OUT = out_kind_of<T>();
   constexpr int32_t kTileCols = BACK ? 256 : 128;  // of an output
+  constexpr bool kScaled = BACK && std::is_same<T, __half>::value;  // (GatedRange)
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -262,6 +264,8 @@ __global__ void __launch_bounds__(PairLayout::kThreads, 1)
           }
         } else {
           const CUtensorMap* mapA = &maps.across[t.which - 1];
+          if constexpr (kScaled)
+            if (__ldcg(p.range.copied + t.m_blk)) mapA = &maps.scaled[t.which - 1];
           for (int32_t i = 0; ok && i < t.k_blocks; ++i)
             ok = fill([&](uint32_t a, uint32_t b, uint32_t bar) {
               tma_load_2d_pair_elect(b, &maps.x, b0, i * kBlockK, bar);
@@ -409,10 +413,19 @@ __global__ void __launch_bounds__(PairLayout::kThreads, 1)
     for (; next(w); ++iter) {
       const GatedTile t(w.u, p, BACK);
       const uint32_t slot = iter & 1u;
+      const int32_t m0 = t.m_blk * 256 + (int32_t)(rank * 128 + q * 32);
+      [[maybe_unused]] float back = 1.0f;  // what takes the scale of this lane's row back, asked for early
+      if constexpr (kScaled) {
+        const int32_t m = m0 + (int32_t)lane, rows = p.product[t.which == 0 ? 0 : 1].M;
+        if (m < rows) {
+          const int64_t i = t.which == 0 ? m : p.range.first_column + (int64_t)(t.which - 1) * rows + m;
+          back = __ldcg(p.range.back + i);
+          if (h == 0 && t.n_blk == 0 && t.slice == 0) p.range.most[i] = 0;  // (the next call's)
+        }
+      }
       if (!warp_wait_inl(acc_full_bar(slot), (iter >> 1) & 1u, ctl, kSiteAccFull)) break;
       tc_fence_after();
       const uint32_t at = tmem + ((q * 32u) << 16) + slot * 256;
-      const int32_t m0 = t.m_blk * 256 + (int32_t)(rank * 128 + q * 32);
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
@@ -451,11 +464,19 @@ __global__ void __launch_bounds__(PairLayout::kThreads, 1)
       } else {
         const int32_t n0 = t.n_blk * kTileCols + (int32_t)h * 128;
         const bool cut = p.slices > 1 && t.which == 0;
+        auto scale_back = [&] {
+          if constexpr (kScaled) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j] *= back;
+          }
+        };
         fetch(at + h * 128, v);
+        scale_back();
         if (cut) leave(v, t.slice, 0, m0, n0);
         else emit(v, t.which, m0, n0);
         fetch(at + h * 128 + 64, v);
         release();
+        scale_back();
         if (cut) leave(v, t.slice, 0, m0, n0 + 64);
         else emit(v, t.which, m0, n0 + 64);
       }
@@ -761,36 +782,197 @@ __device__ __forceinline__ Pack<T, 8> eight_at(const T* at, const T* begin, cons
   }
 }
 
+// Row m's dG and dU from column n on, zeros behind the N-th.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kSlopeThreads) gated_slope_kernel(const GatedSlopeParams p) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const uint32_t per_row = (uint32_t)p.pitch / 8;
-  const int64_t most = p.M * p.N;
+__device__ __forceinline__ void slopes_at(const GatedSlopeParams& p, int64_t m, int32_t n, float (&dg)[8],
+                                          float (&du)[8]) {
+  const int64_t most = p.M * p.N, at = m * p.N + n;
   const T* dh_in = static_cast<const T*>(p.dh);
   const T* gate_in = static_cast<const T*>(p.gate);
   const T* up_in = static_cast<const T*>(p.up);
+  float dh[8], g[8], up[8];
+  unpack(eight_at<T, VEC>(dh_in + at, dh_in, dh_in + most), dh);
+  unpack(eight_at<T, VEC>(gate_in + at, gate_in, gate_in + most), g);
+  unpack(eight_at<T, VEC>(up_in + at, up_in, up_in + most), up);
+  by_kind(p.act, [&](auto kind) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 a = gate_and_slope<decltype(kind)::value>(g[j]);
+      dg[j] = VEC || n + j < p.N ? dh[j] * up[j] * a.y : 0.0f;
+      du[j] = VEC || n + j < p.N ? dh[j] * a.x : 0.0f;
+    }
+  });
+}
+
+// f(row, column) of this thread's vectors.
+template <typename F>
+__device__ __forceinline__ void each_vector(const GatedSlopeParams& p, F f) {
+  const uint32_t per_row = (uint32_t)p.pitch / 8;
   for (int64_t c = (int64_t)blockIdx.x * kSlopeThreads; c < p.M * per_row; c += (int64_t)gridDim.x * kSlopeThreads) {
     const int64_t m0 = c / per_row;  // (of the CTA's first vector)
     const uint32_t i = (uint32_t)(c - m0 * per_row) + threadIdx.x, down = i / per_row;
     const int64_t m = m0 + down;
     if (m >= p.M) break;
-    const int32_t n = (int32_t)(i - down * per_row) * 8;
-    const int64_t at = m * p.N + n;
-    float dh[8], g[8], up[8], dg[8], du[8];
-    unpack(eight_at<T, VEC>(dh_in + at, dh_in, dh_in + most), dh);
-    unpack(eight_at<T, VEC>(gate_in + at, gate_in, gate_in + most), g);
-    unpack(eight_at<T, VEC>(up_in + at, up_in, up_in + most), up);
-    by_kind(p.act, [&](auto kind) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 a = gate_and_slope<decltype(kind)::value>(g[j]);
-        dg[j] = VEC || n + j < p.N ? dh[j] * up[j] * a.y : 0.0f;
-        du[j] = VEC || n + j < p.N ? dh[j] * a.x : 0.0f;
-      }
-    });
+    f(m, (int32_t)(i - down * per_row) * 8);
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kSlopeThreads) gated_slope_kernel(const GatedSlopeParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  each_vector(p, [&](int64_t m, int32_t n) {
+    float dg[8], du[8];
+    slopes_at<T, VEC>(p, m, n, dg, du);
     store_f32<T, 8>(static_cast<T*>(p.dgate) + m * p.pitch + n, dg);
     store_f32<T, 8>(static_cast<T*>(p.dup) + m * p.pitch + n, du);
+  });
+}
+
+// fp16 (GatedRange): the same, unscaled, with the largest magnitudes of rows and columns.  A warp takes
+// 256 columns of every eighth row of its CTA's: a row's largest is one reduction of the warp, a
+// column's stays in a lane's registers; both meet the other CTAs' in memory, where the products leave
+// zeros for the next call.  Measured, with the kernel behind it: 1025 x 1401 9.4 + 4.5 us each alone
+// (the kernel above 6.2), the whole gradients 29.2 -> 34.5 us, 38.7 where rows and columns are scaled;
+// 1024 x 4096 x 2048 50 -> 58 and 68; 8192 x 14336 x 4096 2320 -> 2350 and 2780.
+constexpr int kRangeColumns = 256, kRangeWarps = kSlopeThreads / 32;
+
+// 1 / scale of a row or column.
+__device__ __forceinline__ float back_of(uint32_t most) {
+  if (most == 0 || (most >= __float_as_uint(0x1p-4f) && most < __float_as_uint(0x1p15f))) return 1.0f;
+  return __uint_as_float((max(most >> 23, 27u) - 14u) << 23);
+}
+__device__ __forceinline__ float scale_of(float back) {  // (a power of two's inverse)
+  return __uint_as_float((254u << 23) - __float_as_uint(back));
+}
+
+// A CTA's and a lane's place in both kernels.
+struct RangePlace {
+  int32_t block, stripe, n0, n;
+  int64_t first;  // the warp's first row
+  __device__ __forceinline__ explicit RangePlace(const GatedSlopeParams& p) {
+    const uint32_t stripes = (uint32_t)(p.pitch + kRangeColumns - 1) / kRangeColumns;
+    block = (int32_t)(blockIdx.x / stripes);
+    stripe = (int32_t)(blockIdx.x - (uint32_t)block * stripes);
+    n0 = stripe * kRangeColumns;
+    n = n0 + ((int)threadIdx.x & 31) * 8;
+    first = (int64_t)block * kRangeWarps * p.row_steps + ((int)threadIdx.x >> 5);
+  }
+};
+
+template <int VEC>
+__global__ void __launch_bounds__(kSlopeThreads) gated_slope_range_kernel(const GatedSlopeParams p) {
+  __shared__ alignas(16) uint32_t columns[kRangeWarps][2][kRangeColumns];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const RangePlace at(p);
+  const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t n = at.n;
+  uint32_t of_g[8] = {}, of_u[8] = {};
+  auto larger = [](uint32_t most, float v) {
+    const uint32_t bits = __float_as_uint(v) & 0x7FFFFFFFu;
+    return bits < 0x7F800000u ? max(most, bits) : most;
+  };
+#pragma unroll 2
+  for (int32_t step = 0; step < p.row_steps; ++step) {
+    const int64_t m = at.first + (int64_t)step * kRangeWarps;
+    if (m >= p.M) break;
+    uint32_t most = 0;
+    if (n < p.pitch) {
+      float dg[8], du[8];
+      slopes_at<__half, VEC>(p, m, n, dg, du);
+      store_f32<__half, 8>(static_cast<__half*>(p.dgate) + m * p.pitch + n, dg);
+      store_f32<__half, 8>(static_cast<__half*>(p.dup) + m * p.pitch + n, du);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        of_g[j] = larger(of_g[j], dg[j]), of_u[j] = larger(of_u[j], du[j]);
+        most = larger(larger(most, dg[j]), du[j]);
+      }
+    }
+    if (p.range.rows) {
+      most = __reduce_max_sync(0xFFFFFFFFu, most);
+      if (lane == 0 && most > 0) atomicMax(p.range.most + m, most);
+    }
+  }
+  if (p.range.columns) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      *reinterpret_cast<uint4*>(&columns[warp][0][lane * 8 + j]) = make_uint4(of_g[j], of_g[j + 1], of_g[j + 2], of_g[j + 3]);
+      *reinterpret_cast<uint4*>(&columns[warp][1][lane * 8 + j]) = make_uint4(of_u[j], of_u[j + 1], of_u[j + 2], of_u[j + 3]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int w = 0; w < kRangeWarps; ++w) most = max(most, columns[w][k][tid]);
+      const int32_t c = at.n0 + tid;
+      if (most > 0 && c < p.N) atomicMax(p.range.most + p.range.first_column + (int64_t)k * p.N + c, most);
+    }
+  }
+}
+
+// ... the scales, and what has to be scaled, written, by CTAs of the same places: rows where their others
+// are; a stripe's columns in their own copy, all of them once one of them or any row is scaled.  Mostly
+// nothing has to be.
+template <int VEC>
+__global__ void __launch_bounds__(kSlopeThreads) gated_slope_scale_kernel(const GatedSlopeParams p) {
+  __shared__ float scales[2][kRangeColumns];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const RangePlace at(p);
+  const GatedRange& r = p.range;
+  const int tid = (int)threadIdx.x, lane = tid & 31;
+  // this warp's rows, one for each lane
+  const int64_t own = at.first + (int64_t)lane * kRangeWarps;
+  float row = 1.0f;
+  if (r.rows && lane < p.row_steps && own < p.M) {
+    row = back_of(__ldcg(r.most + own));
+    if (at.stripe == 0) r.back[own] = row;
+  }
+  bool copied = false;
+  if (r.columns) {
+    bool off = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int32_t c = at.n0 + tid;
+      const int64_t i = r.first_column + (int64_t)k * p.N + c;
+      const float back = c < p.N ? back_of(__ldcg(r.most + i)) : 1.0f;
+      if (c < p.N && at.block == 0) r.back[i] = back;
+      scales[k][tid] = scale_of(back);
+      off |= back != 1.0f;
+    }
+    if (r.rows) {
+#pragma unroll 4
+      for (int32_t q = tid; q < r.first_column / 4; q += kSlopeThreads) {
+        const uint4 most = __ldcg(reinterpret_cast<const uint4*>(r.most) + q);
+        off |= back_of(most.x) != 1.0f || back_of(most.y) != 1.0f || back_of(most.z) != 1.0f || back_of(most.w) != 1.0f;
+      }
+    }
+    copied = __syncthreads_or(off) != 0;
+    if (at.block == 0 && tid == 0) r.copied[at.stripe] = copied;
+  }
+  if (copied || __any_sync(0xFFFFFFFFu, row != 1.0f)) {
+    for (int32_t step = 0; step < p.row_steps; ++step) {
+      const int64_t m = at.first + (int64_t)step * kRangeWarps;
+      const float back = __shfl_sync(0xFFFFFFFFu, row, step);
+      if (m >= p.M || at.n >= p.pitch || (!copied && back == 1.0f)) continue;
+      float dg[8], du[8], g[8], u[8];
+      slopes_at<__half, VEC>(p, m, at.n, dg, du);
+      if (back != 1.0f) {
+        const float s = scale_of(back);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = dg[j] * s, u[j] = du[j] * s;
+        store_f32<__half, 8>(static_cast<__half*>(p.dgate) + m * p.pitch + at.n, g);
+        store_f32<__half, 8>(static_cast<__half*>(p.dup) + m * p.pitch + at.n, u);
+      }
+      if (copied) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = dg[j] * scales[0][lane * 8 + j], u[j] = du[j] * scales[1][lane * 8 + j];
+        store_f32<__half, 8>(static_cast<__half*>(p.dgate_by_column) + m * p.pitch + at.n, g);
+        store_f32<__half, 8>(static_cast<__half*>(p.dup_by_column) + m * p.pitch + at.n, u);
+      }
+    }
   }
 }
 
@@ -927,13 +1109,24 @@ cudaError_t launch_rank(GatedRankParams& p, int sms, cudaStream_t stream) {
                     : cudaLaunchKernelEx(&cfg, gated_rank_kernel<T, 8>, p);
 }
 
-template <typename T, int VEC>
-cudaError_t launch_slope(const GatedSlopeParams& p, int sms, cudaStream_t stream) {
+template <int VEC>
+cudaError_t launch_slope(int elem, GatedSlopeParams& p, int sms, cudaStream_t stream) {
   const int64_t want = (p.M * (p.pitch / 8) + kSlopeThreads - 1) / kSlopeThreads;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config_of((unsigned)std::min<int64_t>(want, (int64_t)sms * 16),
-                                           kSlopeThreads, 0, stream, attr, 1);
-  return cudaLaunchKernelEx(&cfg, gated_slope_kernel<T, VEC>, p);
+  cudaLaunchConfig_t cfg = config_of((unsigned)std::min<int64_t>(want, (int64_t)sms * 16), kSlopeThreads, 0, stream, attr, 1);
+  if (elem == kElemBF16) return cudaLaunchKernelEx(&cfg, gated_slope_kernel<__nv_bfloat16, VEC>, p);
+  // rows of a warp: as many as leave every SM four CTAs, 32 at most; of those behind it, which mostly do
+  // next to nothing, two (1025 x 1401, alone, 7.2 us with eight, 4.9 with two)
+  const int64_t stripes = (p.pitch + kRangeColumns - 1) / kRangeColumns, eights = (p.M + kRangeWarps - 1) / kRangeWarps;
+  auto steps = [&](int64_t per_sm) {
+    p.row_steps = (int32_t)std::max<int64_t>(1, std::min<int64_t>(32, eights * stripes / (per_sm * sms)));
+    cfg.gridDim.x = (unsigned)((eights + p.row_steps - 1) / p.row_steps * stripes);
+  };
+  steps(4);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gated_slope_range_kernel<VEC>, p);
+  if (e != cudaSuccess) return e;
+  steps(2);
+  return cudaLaunchKernelEx(&cfg, gated_slope_scale_kernel<VEC>, p);
 }
 
 }  // namespace
@@ -1022,11 +1215,8 @@ cudaError_t launch_gated_rank(int elem, GatedRankParams p, int sms, cudaStream_t
   return elem == kElemF16 ? launch_rank<__half>(p, sms, stream) : launch_rank<__nv_bfloat16>(p, sms, stream);
 }
 
-cudaError_t launch_gated_slope(int elem, const GatedSlopeParams& p, int sms, cudaStream_t stream) {
-  if (elem == kElemF16)
-    return p.vec ? launch_slope<__half, 1>(p, sms, stream) : launch_slope<__half, 0>(p, sms, stream);
-  return p.vec ? launch_slope<__nv_bfloat16, 1>(p, sms, stream)
-               : launch_slope<__nv_bfloat16, 0>(p, sms, stream);
+cudaError_t launch_gated_slope(int elem, GatedSlopeParams p, int sms, cudaStream_t stream) {
+  return p.vec ? launch_slope<1>(elem, p, sms, stream) : launch_slope<0>(elem, p, sms, stream);
 }
 
 }  // namespace gb300

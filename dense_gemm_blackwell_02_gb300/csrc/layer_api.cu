@@ -331,16 +331,34 @@ gemm_status_t gemm_run_gated_grad(gemm_handle_t h, const void* X, const void* ga
   p.slices = gated_slices(p.product[0], sums, 1, others, h->sms);
   p.partial_pitch = (int32_t)K;
   const size_t partial = p.slices > 1 ? (size_t)p.slices * M * K * sizeof(float) : 0;
-  const gemm_status_t st = ensure_scratch(h, 2 * bytes + partial, 0);
+  // fp16: what belongs to the scales, and a copy by columns beside the one by rows
+  const bool scaled = dtype == GEMM_F16;
+  const int copies = scaled && dX && dWg ? 2 : 1;
+  const int64_t first_column = ceil_div(M, 4) * 4, lines = first_column + 2 * N;
+  const size_t ranges = scaled ? (size_t)(lines + ceil_div(N, 256)) * sizeof(float) : 0;
+  const gemm_status_t st =
+      ensure_scratch(h, 2 * copies * bytes + round_up(partial) + ranges, scaled ? (size_t)lines : 0);
   if (st != GEMM_OK) return st;
-  p.partial = reinterpret_cast<float*>(static_cast<char*>(h->op.ptr) + 2 * bytes);
+  char* scratch = static_cast<char*>(h->op.ptr);
+  p.partial = reinterpret_cast<float*>(scratch + 2 * copies * bytes);
   GatedSlopeParams s;
   std::memset(&s, 0, sizeof(s));
   s.dh = g->dH;
   s.gate = g->gate;
   s.up = g->up;
-  s.dgate = h->op.ptr;
-  s.dup = static_cast<char*>(h->op.ptr) + bytes;
+  s.dgate = scratch;
+  s.dup = scratch + bytes;
+  s.dgate_by_column = scratch + 2 * (copies - 1) * bytes;
+  s.dup_by_column = scratch + (2 * copies - 1) * bytes;
+  if (scaled) {
+    s.range.most = static_cast<uint32_t*>(h->op_ctr.ptr);
+    s.range.back = reinterpret_cast<float*>(scratch + 2 * copies * bytes + round_up(partial));
+    s.range.copied = reinterpret_cast<uint32_t*>(s.range.back + lines);
+    s.range.first_column = first_column;
+    s.range.rows = dX != nullptr;
+    s.range.columns = dWg != nullptr;
+    p.range = s.range;
+  }
   s.M = M;
   s.N = (int32_t)N;
   s.pitch = (int32_t)pitch;
@@ -357,6 +375,8 @@ gemm_status_t gemm_run_gated_grad(gemm_handle_t h, const void* X, const void* ga
     return GEMM_ERR_CUDA;
   if (dWg && (!make_map(h, s.dgate, M, pitch, dtype, 64, &maps.across[0]) ||
               !make_map(h, s.dup, M, pitch, dtype, 64, &maps.across[1]) ||
+              (scaled && (!make_map(h, s.dgate_by_column, M, pitch, dtype, 64, &maps.scaled[0]) ||
+                          !make_map(h, s.dup_by_column, M, pitch, dtype, 64, &maps.scaled[1]))) ||
               !make_map(h, X, M, K, dtype, 64, &maps.x) ||
               !make_map(h, dWg, N, K, dtype, 32, &maps.out[1]) ||
               !make_map(h, dWu, N, K, dtype, 32, &maps.out[2])))
@@ -370,7 +390,10 @@ gemm_status_t gemm_run_gated_grad(gemm_handle_t h, const void* X, const void* ga
 
   gemm_status_t done = few ? launched(h, launch_gated_rank(dtype, r, h->sms, stream)) : GEMM_OK;
   if (done == GEMM_OK) done = launched(h, launch_gated_slope(dtype, s, h->sms, stream));
-  if (done == GEMM_OK) done = launched(h, launch_gated(true, dtype, maps, p, h->sms, stream));
+  if (done != GEMM_OK) return done;
+  done = launched(h, launch_gated(true, dtype, maps, p, h->sms, stream));
+  // (what the products would have left zero)
+  if (done != GEMM_OK && scaled) cudaMemsetAsync(s.range.most, 0, (size_t)lines * sizeof(uint32_t), stream);
   if (done == GEMM_OK && p.slices > 1) done = launched(h, launch_gated_join(true, dtype, p, stream));
   return done;
 }

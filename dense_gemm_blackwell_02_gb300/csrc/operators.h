@@ -146,6 +146,7 @@ enum GateKind : int { kGateSilu = 0, kGateGelu = 1, kGateGeluTanh = 2, kGateRelu
 struct GatedMaps {
   CUtensorMap a[2];       // X; dG, dU: box {64, 128}
   CUtensorMap across[2];  // dG, dU: box {64, 64}
+  CUtensorMap scaled[2];  // fp16: the same scaled by columns (GatedRange)
   CUtensorMap b[2];       // Wg, Wu: box {64, 128}, backwards {64, 64}
   CUtensorMap x;          // X: box {64, 64}
   CUtensorMap out[3];     // box {64, 32}
@@ -156,6 +157,19 @@ struct GatedProduct {
   int32_t tiles;
   int32_t k_blocks;       // of one pair of operands
 };
+// fp16's range is too short for dG and dU (products of two values and a slope): a row of both, for dX,
+// and a column of either, for the weights' gradients, whose largest finite value lies outside
+// 2^-4..2^15 is scaled by the power of two that brings it to 2^14..2^15, and its sums are scaled back.
+// 2^-4 leaves a term an error of 2^-21 of that largest, if not of half its own step.
+struct GatedRange {
+  uint32_t* most;         // magnitudes' bit patterns: of M rows, from first_column on of dG's and of
+                          // dU's N columns; zero between calls
+  float* back;            // 1 / scale, laid out as `most`
+  uint32_t* copied;       // of 256 columns each: in use is their scaled copy
+  int64_t first_column;   // M rounded up to 4
+  int32_t rows, columns;  // wanted (dX, the weights' gradients)
+};
+
 struct GatedParams {
   void* out[3];           // H, gate, up; dX, dWg, dWu: row-major, dense
   int32_t outs;           // forwards: how many of them
@@ -168,6 +182,7 @@ struct GatedParams {
   int32_t group_m;        // grouped rasterisation: tiles along M per group
   int32_t act;            // GateKind
   int32_t tma_store;      // the outputs are written through their maps
+  GatedRange range;       // backwards in fp16
   uint32_t* status;
   uint64_t wait_limit_ns;
   int32_t test_stall;
@@ -223,8 +238,13 @@ struct GatedSlopeParams {
   int32_t N, pitch;
   int32_t act;
   int32_t vec;           // N is a multiple of 8 and the inputs start on 16 bytes
+  // fp16
+  GatedRange range;
+  void* dgate_by_column; // where dG and dU scaled by columns go: dgate and dup if rows are not wanted
+  void* dup_by_column;
+  int32_t row_steps;     // filled in by the launch: rows of a warp
 };
-cudaError_t launch_gated_slope(int elem, const GatedSlopeParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_gated_slope(int elem, GatedSlopeParams p, int sms, cudaStream_t stream);
 
 // dWg and dWu of up to kGatedRankRows rows, dG and dU unrounded.
 constexpr int32_t kGatedRankRows = 8;

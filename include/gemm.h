@@ -672,8 +672,12 @@ gemm_status_t gemm_run_gated(gemm_handle_t h, const void* X, const void* gate_we
  *                                 be NULL).  Overwritten, not added to
  * All of `dtype`.  dG and dU are rounded to it (the matrix instructions' operands; up to eight
  * rows enter the weights' gradients unrounded), sums are in binary32, results are rounded
- * once.  No output may overlap an input or another output.  The handle keeps 4 M N bytes of
- * scratch, and up to 20 MB more.  A gradient is the same bits whichever others are asked for.
+ * once.  In fp16 dG and dU may leave its range: rows of them (for dX) and columns (for the
+ * weights' gradients) are scaled by powers of two where their largest lies outside 2^-4..2^15, so
+ * that a term is off by half a step of itself, or by 2^-21 of its row's or column's largest where
+ * that is more.  No output may overlap an input or another output.  The handle keeps 4 M N bytes
+ * of scratch (8 M N in fp16 for all three gradients), and up to 20 MB and 8 (M + 2 N) bytes more.
+ * A gradient is the same bits whichever others are asked for.
  * M == 0 or N == 0 gives zeros (sums of nothing); act' of
  * GEMM_GATE_RELU is 0 at 0.
  */
