@@ -832,9 +832,11 @@ __global__ void __launch_bounds__(kSlopeThreads) gated_slope_kernel(const GatedS
 // fp16 (GatedRange): the same, unscaled, with the largest magnitudes of rows and columns.  A warp takes
 // 256 columns of every eighth row of its CTA's: a row's largest is one reduction of the warp, a
 // column's stays in a lane's registers; both meet the other CTAs' in memory, where the products leave
-// zeros for the next call.  Measured, with the kernel behind it: 1025 x 1401 9.4 + 4.5 us each alone
-// (the kernel above 6.2), the whole gradients 29.2 -> 34.5 us, 38.7 where rows and columns are scaled;
-// 1024 x 4096 x 2048 50 -> 58 and 68; 8192 x 14336 x 4096 2320 -> 2350 and 2780.
+// zeros for the next call.  (An infinity may be the largest: what its row's or column's others are
+// then scaled to does not matter, because the sums are infinite or NaN, and a NaN is none.)
+// Measured, with the kernel behind it: 1025 x 1401 8.9 and 4.3 us each alone (the kernel above 6.2), the
+// whole gradients 29 -> 34 us, 38.4 where rows and columns are scaled; 1024 x 4096 x 2048 50 -> 57 and
+// 67; 8192 x 14336 x 4096 within the spread of 2300 to 2390, and 2720 to 2790.
 constexpr int kRangeColumns = 256, kRangeWarps = kSlopeThreads / 32;
 
 // 1 / scale of a row or column.
@@ -861,23 +863,19 @@ struct RangePlace {
 };
 
 template <int VEC>
-__global__ void __launch_bounds__(kSlopeThreads) gated_slope_range_kernel(const GatedSlopeParams p) {
-  __shared__ alignas(16) uint32_t columns[kRangeWarps][2][kRangeColumns];
+__global__ void __launch_bounds__(kSlopeThreads, 4) gated_slope_range_kernel(const GatedSlopeParams p) {
+  __shared__ alignas(16) float columns[kRangeWarps][2][kRangeColumns];
   grid_dependency_wait();
   grid_launch_dependents();
   const RangePlace at(p);
   const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t n = at.n;
-  uint32_t of_g[8] = {}, of_u[8] = {};
-  auto larger = [](uint32_t most, float v) {
-    const uint32_t bits = __float_as_uint(v) & 0x7FFFFFFFu;
-    return bits < 0x7F800000u ? max(most, bits) : most;
-  };
+  float of_g[8] = {}, of_u[8] = {};
 #pragma unroll 2
   for (int32_t step = 0; step < p.row_steps; ++step) {
     const int64_t m = at.first + (int64_t)step * kRangeWarps;
     if (m >= p.M) break;
-    uint32_t most = 0;
+    float most = 0.0f;
     if (n < p.pitch) {
       float dg[8], du[8];
       slopes_at<__half, VEC>(p, m, n, dg, du);
@@ -885,29 +883,30 @@ __global__ void __launch_bounds__(kSlopeThreads) gated_slope_range_kernel(const 
       store_f32<__half, 8>(static_cast<__half*>(p.dup) + m * p.pitch + n, du);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        of_g[j] = larger(of_g[j], dg[j]), of_u[j] = larger(of_u[j], du[j]);
-        most = larger(larger(most, dg[j]), du[j]);
+        of_g[j] = fmaxf(of_g[j], fabsf(dg[j])), of_u[j] = fmaxf(of_u[j], fabsf(du[j]));
+        most = fmaxf(most, fmaxf(fabsf(dg[j]), fabsf(du[j])));
       }
     }
     if (p.range.rows) {
-      most = __reduce_max_sync(0xFFFFFFFFu, most);
-      if (lane == 0 && most > 0) atomicMax(p.range.most + m, most);
+      const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+      if (lane == 0 && bits > 0) atomicMax(p.range.most + m, bits);
     }
   }
   if (p.range.columns) {
 #pragma unroll
     for (int j = 0; j < 8; j += 4) {
-      *reinterpret_cast<uint4*>(&columns[warp][0][lane * 8 + j]) = make_uint4(of_g[j], of_g[j + 1], of_g[j + 2], of_g[j + 3]);
-      *reinterpret_cast<uint4*>(&columns[warp][1][lane * 8 + j]) = make_uint4(of_u[j], of_u[j + 1], of_u[j + 2], of_u[j + 3]);
+      *reinterpret_cast<float4*>(&columns[warp][0][lane * 8 + j]) = make_float4(of_g[j], of_g[j + 1], of_g[j + 2], of_g[j + 3]);
+      *reinterpret_cast<float4*>(&columns[warp][1][lane * 8 + j]) = make_float4(of_u[j], of_u[j + 1], of_u[j + 2], of_u[j + 3]);
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      uint32_t most = 0;
+      float most = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kRangeWarps; ++w) most = max(most, columns[w][k][tid]);
+      for (int w = 0; w < kRangeWarps; ++w) most = fmaxf(most, columns[w][k][tid]);
       const int32_t c = at.n0 + tid;
-      if (most > 0 && c < p.N) atomicMax(p.range.most + p.range.first_column + (int64_t)k * p.N + c, most);
+      if (most > 0.0f && c < p.N)
+        atomicMax(p.range.most + p.range.first_column + (int64_t)k * p.N + c, __float_as_uint(most));
     }
   }
 }

@@ -158,7 +158,7 @@ struct GatedProduct {
   int32_t k_blocks;       // of one pair of operands
 };
 // fp16's range is too short for dG and dU (products of two values and a slope): a row of both, for dX,
-// and a column of either, for the weights' gradients, whose largest finite value lies outside
+// and a column of either, for the weights' gradients, whose largest lies outside
 // 2^-4..2^15 is scaled by the power of two that brings it to 2^14..2^15, and its sums are scaled back.
 // 2^-4 leaves a term an error of 2^-21 of that largest, if not of half its own step.
 struct GatedRange {
