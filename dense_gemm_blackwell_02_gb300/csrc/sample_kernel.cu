@@ -43,8 +43,8 @@
 // Measured: one row of 128256 bf16 10 us without limits, 15 with top-k 50, 40 with top-p 0.9 or
 // 0.99 of a flat row: the latency of its passes and of the cluster's barriers between them, about
 // 1.5 us each.
-// 256 rows of 128256 fp32 (19 us at HBM's rate): 57 us greedy, 90 without limits, 81 with top-k
-// 50, 262 with top-p 0.9, 129 with mixed limits: three to four rounds of 72 rows, each of which
+// 256 rows of 128256 fp32 (19 us at HBM's rate): 57 us greedy, 87 to 93 without limits, 81 with top-k
+// 50, 266 with top-p 0.9, 130 with mixed limits, 676 with top-p 0.9 after top-k 20000: three to four rounds of 72 rows, each of which
 // waits for its own passes; memory is read ahead for the next round.
 #include <algorithm>
 #include <cmath>
@@ -1553,7 +1553,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   part.resident = p.resident != 0;
 
   // The row that will run here after this one is brought into L2 meanwhile, so that memory is read
-  // also while the rows here are worked on, 8 KB by each instruction.
+  // also while the rows here are worked on.  8 KB by each instruction, so that several threads ask for a
+  // slice: nothing requires that size, and larger pieces have not been measured.
   if (next < p.rows && part.n > 0) {
     constexpr uintptr_t kAhead = 8192;
     const uintptr_t from = reinterpret_cast<uintptr_t>(part.in + (int64_t)(next - row) * p.stride);

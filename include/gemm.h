@@ -775,7 +775,7 @@ gemm_status_t gemm_norm_rotary_grad(gemm_handle_t h, const void* x, const void* 
  * have logits further from m than binary32's largest number.  A w below 2^-60 counts as 0; every
  * other one counts, also where random is 0 or 1.  Where the result hangs on a border between two
  * tokens, weights good to 2^-34 decide, so that it is the formula's unless a running sum lies
- * within 2^-33 of the whole from the border, and the same from run to run.
+ * within 2^-30 of the whole from the border, and the same from run to run.
  * logits: rows x vocab with a row stride in elements; device memory, like all vectors (one
  * value per row), none of which may change while the call runs.  tokens and probs may not
  * overlap each other or an input.
